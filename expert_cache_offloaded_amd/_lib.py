@@ -15,7 +15,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmc.so")
 
 MC_OK, MC_EINVAL, MC_ENOMEM, MC_EHIP, MC_EUNSUPPORTED, MC_EDEVICE = 0, -1, -2, -3, -4, -5
-MC_BF16, MC_MXFP4 = 0, 1
+MC_BF16, MC_MXFP4, MC_F32, MC_F16 = 0, 1, 2, 3
 MC_SPLIT_SUBMIT, MC_MERGE = 0, 1
 FMT = {"bf16": MC_BF16, "mxfp4": MC_MXFP4}
 STAT_NAMES = ("hits", "misses", "fills", "host", "evictions", "calls", "err", "reserved")
@@ -69,8 +69,19 @@ class Hybrid(C.Structure):
                 ("y_host", C.c_void_p), ("y_bf16", C.c_void_p)]
 
 
+class Grouped(C.Structure):
+    _fields_ = [("x_fmt", C.c_int32), ("w_fmt", C.c_int32), ("y_fmt", C.c_int32), ("swiglu", C.c_int32),
+                ("E", C.c_int32), ("M", C.c_int32), ("N", C.c_int32), ("K", C.c_int32),
+                ("x_rows", C.c_int32), ("x_div", C.c_int32), ("y_rows", C.c_int32), ("x_perm", C.c_int32),
+                ("y_perm", C.c_int32), ("n_gate", C.c_int32), ("ldx", C.c_int64), ("ldy", C.c_int64),
+                ("n", C.c_int64), ("x", C.c_void_p), ("x_scale", C.c_void_p), ("w", C.c_void_p),
+                ("w_scale", C.c_void_p), ("y", C.c_void_p), ("y_scale", C.c_void_p), ("offsets", C.c_void_p),
+                ("perm", C.c_void_p), ("entry_of", C.c_void_p), ("gate", C.c_void_p)]
+
+
 _P = C.c_void_p
 _I32 = C.c_int32
+_I64 = C.c_int64
 _SIGS = {
     "mc_abi_version": (C.c_int, []),
     "mc_last_error": (C.c_char_p, []),
@@ -98,6 +109,13 @@ _SIGS = {
     "moe_experts_prefill_part": (C.c_int, [_P, _P, _P, _I32, _I32, _P, _I32, C.POINTER(Banks), _P, _I32, _P,
                                            C.c_size_t, _P, _P, _P]),
     "moe_experts_prefill_status": (C.c_int, [_P, _P, C.POINTER(C.c_uint32)]),
+    "mc_mxfp4_quantize": (C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P]),
+    "mc_mxfp4_dequantize": (C.c_int, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
+    "mc_mxfp4_matmul": (C.c_int, [_P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _P, _I32, _I64, _P]),
+    "mc_grouped_matmul": (C.c_int, [C.POINTER(Grouped), _P]),
+    "moe_experts_prefill_act_ws_bytes": (C.c_size_t, [_I32, _I32, _I32, _I32, _I32, _I32]),
+    "moe_experts_prefill_act": (C.c_int, [_P, _P, _P, _I32, _I32, _P, _I32, C.POINTER(Banks), _I32, _P,
+                                          C.c_size_t, _P, _P, C.POINTER(Prefetch)]),
     "mc_host_pool_create": (_P, [_I32, _P]),
     "mc_host_pool_destroy": (None, [_P]),
     "mc_host_pool_cpus": (C.c_int32, [_P, _P, _I32]),
@@ -351,6 +369,216 @@ def moe_experts_prefill_part(x, ids, w, n_tok, E: int, part_buf: Banks, entry_of
     _check("moe_experts_prefill_part", lib().moe_experts_prefill_part(
         _ptr(x), _ptr(ids), _ptr(w), T, k, _ptr(n_tok), E, C.byref(part_buf), _ptr(entry_of), steps, _ptr(ws),
         ws.numel() * ws.element_size(), _ptr(counts), _ptr(y), _stream(stream)))
+
+
+# ---------------------------------------------------------------- MXFP4 and grouped products
+
+def _types():
+    import torch
+    return {torch.bfloat16: MC_BF16, torch.int16: MC_BF16, torch.float32: MC_F32, torch.float16: MC_F16,
+            torch.uint8: MC_MXFP4}
+
+
+_type_ids = None
+
+
+def _etype(t) -> int:
+    """Element type of a tensor: bf16 values or their bits (int16), fp32, fp16, MXFP4 codes (uint8)."""
+    global _type_ids
+    if _type_ids is None:
+        _type_ids = _types()
+    try:
+        return _type_ids[t.dtype]
+    except KeyError:
+        raise ValueError("no element type for %s tensors" % t.dtype) from None
+
+
+def _device(fn: str, first, *rest):
+    """The tensors' GPU: all of them on one."""
+    d = first.device
+    if d.type != "cuda" or any(t is not None and t.device != d for t in rest):
+        raise ValueError("%s: tensors must all be on one GPU" % fn)
+    return d
+
+
+def _on(device, stream):
+    """(stream handle, context): the given stream, or the current one of the tensors' GPU, with that
+    GPU current while the call is made."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    ctx = contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return stream.cuda_stream, ctx
+
+
+def _rows(fn: str, what: str, t, cols: int, rows: Optional[int] = None) -> int:
+    """Leading stride of a 2-D tensor of `cols` columns whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
+        raise ValueError("%s: %s has shape %s" % (fn, what, tuple(t.shape)))
+    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError("%s: the rows of %s must be contiguous" % (fn, what))
+    return t.stride(0) if t.shape[0] > 1 else max(cols, 1)
+
+
+def _packed(fn: str, what: str, t, shape, dtype) -> None:
+    """A contiguous tensor of the given shape and type."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s: %s must be a contiguous %s tensor of shape %s, not %s %s"
+                         % (fn, what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+
+
+def _codes(fn: str, what: str, codes, scales) -> int:
+    """Checks MXFP4 codes [..., C/2] with scales [..., C/32]; returns C."""
+    import torch
+    if scales is None:
+        raise ValueError("%s: MXFP4 %s needs its scales" % (fn, what))
+    C_ = 2 * codes.shape[-1]
+    _packed(fn, what, codes, codes.shape, torch.uint8)
+    _packed(fn, what + "'s scales", scales, tuple(codes.shape[:-1]) + (C_ // 32,), torch.uint8)
+    return C_
+
+
+def mxfp4_quantize(src, codes, scales, stream=None) -> None:
+    """Rows of src (bf16, fp16 or fp32 [rows][cols]; rows may lie apart) to MXFP4 codes u8
+    [rows][cols/2] and scales u8 [rows][cols/32]."""
+    cols = _codes("mxfp4_quantize", "codes", codes, scales)
+    ld = _rows("mxfp4_quantize", "src", src, cols, codes.shape[0])
+    d = _device("mxfp4_quantize", src, codes, scales)
+    st, ctx = _on(d, stream)
+    with ctx:
+        _check("mc_mxfp4_quantize", lib().mc_mxfp4_quantize(
+            _ptr(src), _etype(src), src.shape[0], cols, ld if src.shape[0] > 1 else (ld + 7) & ~7, _ptr(codes),
+            _ptr(scales), st))
+
+
+def mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
+    """The values of MXFP4 rows, to dst (bf16, fp16 or fp32 [rows][cols]; rows may lie apart)."""
+    cols = _codes("mxfp4_dequantize", "codes", codes, scales)
+    ld = _rows("mxfp4_dequantize", "dst", dst, cols, codes.shape[0])
+    d = _device("mxfp4_dequantize", dst, codes, scales)
+    st, ctx = _on(d, stream)
+    with ctx:
+        _check("mc_mxfp4_dequantize", lib().mc_mxfp4_dequantize(
+            _ptr(codes), _ptr(scales), codes.shape[0], cols, _ptr(dst), _etype(dst), ld, st))
+
+
+def mxfp4_matmul(x, w, w_scale, y, x_scale=None, stream=None) -> None:
+    """y [M][N] (bf16 or fp32) = x [M][K] times the transpose of the MXFP4 matrix w ([N][K/2] codes,
+    w_scale [N][K/32]).  x: bf16, or MXFP4 codes u8 [M][K/2] with x_scale; the rows of a bf16 x and of
+    y may lie apart."""
+    fn = "mxfp4_matmul"
+    K = _codes(fn, "w", w, w_scale)
+    if w.dim() != 2:
+        raise ValueError("%s: w has shape %s" % (fn, tuple(w.shape)))
+    xf, ldx = _x_operand(fn, x, x_scale, K)
+    ldy = _rows(fn, "y", y, w.shape[0], x.shape[0])
+    d = _device(fn, x, w, w_scale, y, x_scale)
+    st, ctx = _on(d, stream)
+    with ctx:
+        _check("mc_mxfp4_matmul", lib().mc_mxfp4_matmul(
+            _ptr(x), _ptr(x_scale), xf, ldx, _ptr(w), _ptr(w_scale), x.shape[0], w.shape[0], K, _ptr(y),
+            _etype(y), ldy, st))
+
+
+def _x_operand(fn: str, x, x_scale, K: int):
+    xf = _etype(x)
+    if xf == MC_MXFP4:
+        if _codes(fn, "x", x, x_scale) != K or x.dim() != 2:
+            raise ValueError("%s: x has shape %s, w has %d columns" % (fn, tuple(x.shape), K))
+        return xf, K
+    if x_scale is not None:
+        raise ValueError("%s: x_scale belongs to MXFP4 x" % fn)
+    return xf, _rows(fn, "x", x, K)
+
+
+def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, swiglu: bool = False, perm=None,
+                   x_div: int = 1, x_perm: Optional[bool] = None, y_perm: bool = False, gate=None, entry_of=None,
+                   stream=None) -> None:
+    """Products of sorted rows with their group's matrix of w (mc_grouped_matmul): row i of group e
+    (offsets[e] <= i < offsets[e + 1], device int32 [E + 1]) of x times the transpose of
+    w[entry_of[e]], through SwiGLU if asked, times its gate.
+      x         bf16 [rows][K], or MXFP4 codes u8 [rows][K/2] with x_scale
+      w         bf16 [n][N][K], or MXFP4 codes u8 [n][N][K/2] with w_scale
+      y         bf16 or fp32, or MXFP4 codes u8 with y_scale; N columns (N / 2 with swiglu)
+      perm      int32: the route of every sorted row (prefill_sort_routes); x rows are then gathered
+                from perm[i] / x_div (x_perm=False: from i), y rows scattered to perm[i] with y_perm
+      gate      fp32 by route (by row without perm; rows past its end are skipped); entry_of int32 [E], -1 = leave the group out
+    Without perm the number of rows is y's; with it perm's."""
+    import torch
+    fn = "grouped_matmul"
+    if w.dim() != 3:
+        raise ValueError("%s: w has shape %s" % (fn, tuple(w.shape)))
+    wf = _etype(w)
+    K = w.shape[2]
+    if wf == MC_MXFP4:
+        K = _codes(fn, "w", w, w_scale)
+    elif w_scale is not None:
+        raise ValueError("%s: w_scale belongs to MXFP4 w" % fn)
+    elif not w.is_contiguous():
+        raise ValueError("%s: w must be contiguous" % fn)
+    xf, ldx = _x_operand(fn, x, x_scale, K)
+    n_out = w.shape[1] // 2 if swiglu else w.shape[1]
+    yf = _etype(y)
+    ldy = 0
+    if yf == MC_MXFP4:
+        if y.dim() != 2 or _codes(fn, "y", y, y_scale) != n_out:
+            raise ValueError("%s: y has shape %s, the result %d columns" % (fn, tuple(y.shape), n_out))
+    elif y_scale is not None:
+        raise ValueError("%s: y_scale belongs to MXFP4 y" % fn)
+    else:
+        ldy = _rows(fn, "y", y, n_out)
+    E = offsets.shape[0] - 1
+    _packed(fn, "offsets", offsets, (E + 1,), torch.int32)
+    M = y.shape[0]
+    if perm is not None:
+        M = perm.shape[0]
+        _packed(fn, "perm", perm, (M,), torch.int32)
+    if entry_of is not None:
+        _packed(fn, "entry_of", entry_of, (E,), torch.int32)
+    if gate is not None:
+        _packed(fn, "gate", gate, gate.shape, torch.float32)
+    if x_perm is None:
+        x_perm = perm is not None
+    d = _device(fn, x, w, offsets, y, x_scale, w_scale, y_scale, perm, gate, entry_of)
+    g = Grouped(xf, wf, yf, int(bool(swiglu)), E, M, w.shape[1], K, x.shape[0], x_div, y.shape[0], int(bool(x_perm)),
+                int(bool(y_perm)), 0 if gate is None else gate.numel(), ldx, ldy, w.shape[0], _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y),
+                _ptr(y_scale), _ptr(offsets), _ptr(perm), _ptr(entry_of), _ptr(gate))
+    st, ctx = _on(d, stream)
+    with ctx:
+        _check("mc_grouped_matmul", lib().mc_grouped_matmul(C.byref(g), st))
+
+
+def prefill_act_ws_bytes(T: int, k: int, E: int, H: int, I: int, act: str) -> int:
+    return int(lib().moe_experts_prefill_act_ws_bytes(T, k, E, H, I, FMT[act]))
+
+
+def moe_experts_prefill_act(x, ids, w, n_tok, E: int, layer_buf: Banks, act: str, ws, y,
+                            nxt: Optional[Prefetch] = None, stream=None) -> None:
+    """Prefill layer on bf16 or MXFP4 activations (act = "bf16" or "mxfp4"): x and y bf16 (values or
+    bits) [T][H], ids int32 and w fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes."""
+    import torch
+    fn = "moe_experts_prefill_act"
+    if act not in FMT:
+        raise ValueError("%s: act must be bf16 or mxfp4, not %r" % (fn, act))
+    if ids.dim() != 2:
+        raise ValueError("%s: ids has shape %s" % (fn, tuple(ids.shape)))
+    T, k = ids.shape
+    _packed(fn, "ids", ids, (T, k), torch.int32)
+    _packed(fn, "w", w, (T, k), torch.float32)
+    for what, t in (("x", x), ("y", y)):
+        if _etype(t) != MC_BF16:
+            raise ValueError("%s: %s must be bf16, not %s" % (fn, what, t.dtype))
+        _packed(fn, what, t, (T, layer_buf.H), t.dtype)
+    if n_tok is not None:
+        _packed(fn, "n_tok", n_tok, (1,), torch.int32)
+    d = _device(fn, x, ids, w, n_tok, ws, y)
+    st, ctx = _on(d, stream)
+    with ctx:
+        _check(fn, lib().moe_experts_prefill_act(
+            _ptr(x), _ptr(ids), _ptr(w), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], _ptr(ws),
+            ws.numel() * ws.element_size(), _ptr(y), st, C.byref(nxt) if nxt is not None else None))
 
 
 class HostPool:

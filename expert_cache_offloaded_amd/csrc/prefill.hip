@@ -30,6 +30,7 @@
 // block id is remapped so consecutive tiles run on the same XCD (its L2 holds the
 // expert's weights and activation rows while they are reused).
 #include "mc_common.h"
+#include "prefill.h"
 
 namespace mc {
 
@@ -42,7 +43,6 @@ constexpr int kP_Threads = 256;
 constexpr int kP_GU_Cols = 128;    // intermediate columns per gate_up tile (32 per wave)
 constexpr int kP_DN_Cols = 256;    // output columns per down tile (64 per wave)
 constexpr int kP_LdsRow = kP_KS + 8;   // padded LDS row (elements)
-constexpr int kP_MaxE = 1024;
 constexpr int kP_MaxK = 8192;      // largest H or I (sizes the generic kernel's scale table)
 
 // Status bits of a prefill call (the workspace's first word, cleared by the call's first
@@ -641,16 +641,58 @@ prefill_combine_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int
   }
 }
 
-static int sort_launch(const int32_t* ids, int T, int k, const int32_t* n_tok, int E,
-                       const PrefillWs& w, hipStream_t s) {
-  hipLaunchKernelGGL(sort_count_kernel, dim3(E), dim3(256), 0, s, ids, T, k, n_tok, E, w.counts,
-                     w.counts4, w.status);
-  hipLaunchKernelGGL(sort_plan_kernel, dim3(1), dim3(1024), 0, s, E, w.counts, w.offsets,
-                     w.mtile_off, w.tile_e);
-  hipLaunchKernelGGL(sort_scatter_kernel, dim3(E), dim3(256), 0, s, ids, T, k, n_tok, E, w.counts4,
-                     w.offsets, w.perm);
+int sort_routes_launch(const int32_t* ids, int T, int k, const int32_t* n_tok, int E, const SortBuffers& b,
+                       hipStream_t s) {
+  hipLaunchKernelGGL(sort_count_kernel, dim3(E), dim3(256), 0, s, ids, T, k, n_tok, E, b.counts,
+                     b.counts4, b.status);
+  hipLaunchKernelGGL(sort_plan_kernel, dim3(1), dim3(1024), 0, s, E, b.counts, b.offsets,
+                     b.mtile_off, b.tile_e);
+  hipLaunchKernelGGL(sort_scatter_kernel, dim3(E), dim3(256), 0, s, ids, T, k, n_tok, E, b.counts4,
+                     b.offsets, b.perm);
   MC_LAUNCH_CHECK();
   return MC_OK;
+}
+
+int combine_launch(const int32_t* ids, int T, int k, int E, int H, const int32_t* n_tok, const float* yr,
+                   uint16_t* y_bf16, hipStream_t s) {
+  const int64_t n4 = (int64_t)T * H / 4;
+  int64_t gc = (n4 + 255) / 256;
+  if (gc > 8192) gc = 8192;
+  hipLaunchKernelGGL(prefill_combine_kernel, dim3((unsigned)gc), dim3(256), 0, s, ids, T, k, E, H, n_tok, yr, y_bf16);
+  MC_LAUNCH_CHECK();
+  return MC_OK;
+}
+
+int prefetch_launch(const char* fn, const mc_prefetch* next, int E) {
+  int rc;
+  MC_REQUIRE(next->host_src && next->dst && next->copy, "%s: bad prefetch", fn);
+  if ((rc = check_banks(next->host_src, "prefetch host_src")) != MC_OK) return rc;
+  if ((rc = check_banks(next->dst, "prefetch dst")) != MC_OK) return rc;
+  MC_REQUIRE(next->host_src->fmt == next->dst->fmt && next->host_src->H == next->dst->H &&
+                 next->host_src->I == next->dst->I,
+             "%s: prefetch source and destination differ", fn);
+  MC_REQUIRE(next->first_flat >= 0 && next->first_flat + E <= next->host_src->n && next->dst->n >= E,
+             "%s: prefetch range out of bounds", fn);
+  if (next->dst_free) MC_HIP(hipStreamWaitEvent(next->copy, next->dst_free, 0));
+  BankBytes bb = bank_bytes(next->dst->fmt, next->dst->H, next->dst->I);
+  const size_t nbytes[4] = {bb.gate_up, bb.gate_up_scale, bb.down, bb.down_scale};
+  const void* src[4] = {next->host_src->gate_up, next->host_src->gate_up_scale,
+                        next->host_src->down, next->host_src->down_scale};
+  void* dst[4] = {next->dst->gate_up, next->dst->gate_up_scale, next->dst->down,
+                  next->dst->down_scale};
+  for (int b = 0; b < 4; ++b) {
+    if (nbytes[b] == 0) continue;
+    MC_HIP(hipMemcpyAsync(dst[b], static_cast<const uint8_t*>(src[b]) + nbytes[b] * next->first_flat,
+                          nbytes[b] * (size_t)E, hipMemcpyHostToDevice, next->copy));
+  }
+  if (next->done) MC_HIP(hipEventRecord(next->done, next->copy));
+  return MC_OK;
+}
+
+static int sort_launch(const int32_t* ids, int T, int k, const int32_t* n_tok, int E,
+                       const PrefillWs& w, hipStream_t s) {
+  const SortBuffers b{w.counts, w.counts4, w.offsets, w.mtile_off, w.perm, w.tile_e, w.status};
+  return sort_routes_launch(ids, T, k, n_tok, E, b, s);
 }
 
 }  // namespace mc
@@ -744,14 +786,8 @@ static int prefill_steps(const void* x_bf16, const int32_t* ids, const float* w,
       hipLaunchKernelGGL((prefill_gemm_kernel<1, 0>), dim3(g), dim3(kP_Threads), 0, s, a);
     MC_LAUNCH_CHECK();
   }
-  if (steps & MC_PF_COMBINE) {
-    const int64_t n4 = (int64_t)T * H / 4;
-    int64_t gc = (n4 + 255) / 256;
-    if (gc > 8192) gc = 8192;
-    hipLaunchKernelGGL(prefill_combine_kernel, dim3((unsigned)gc), dim3(256), 0, s, ids, T, k, E, H, n_tok, pw.yr,
-                       static_cast<uint16_t*>(y_bf16));
-    MC_LAUNCH_CHECK();
-  }
+  if (steps & MC_PF_COMBINE)
+    return combine_launch(ids, T, k, E, H, n_tok, pw.yr, static_cast<uint16_t*>(y_bf16), s);
   return MC_OK;
 }
 
@@ -766,29 +802,7 @@ extern "C" int moe_experts_prefill(const void* x_bf16, const int32_t* ids, const
              "moe_experts_prefill: x, ws and y must be 16-byte aligned");
 
   // prefetch of the next layer's whole pool on the copy stream (double buffer)
-  if (next) {
-    MC_REQUIRE(next->host_src && next->dst && next->copy, "moe_experts_prefill: bad prefetch");
-    if ((rc = check_banks(next->host_src, "prefetch host_src")) != MC_OK) return rc;
-    if ((rc = check_banks(next->dst, "prefetch dst")) != MC_OK) return rc;
-    MC_REQUIRE(next->host_src->fmt == next->dst->fmt && next->host_src->H == next->dst->H &&
-                   next->host_src->I == next->dst->I,
-               "moe_experts_prefill: prefetch source and destination differ");
-    MC_REQUIRE(next->first_flat >= 0 && next->first_flat + E <= next->host_src->n && next->dst->n >= E,
-               "moe_experts_prefill: prefetch range out of bounds");
-    if (next->dst_free) MC_HIP(hipStreamWaitEvent(next->copy, next->dst_free, 0));
-    BankBytes bb = bank_bytes(next->dst->fmt, next->dst->H, next->dst->I);
-    const size_t nbytes[4] = {bb.gate_up, bb.gate_up_scale, bb.down, bb.down_scale};
-    const void* src[4] = {next->host_src->gate_up, next->host_src->gate_up_scale,
-                          next->host_src->down, next->host_src->down_scale};
-    void* dst[4] = {next->dst->gate_up, next->dst->gate_up_scale, next->dst->down,
-                    next->dst->down_scale};
-    for (int b = 0; b < 4; ++b) {
-      if (nbytes[b] == 0) continue;
-      MC_HIP(hipMemcpyAsync(dst[b], static_cast<const uint8_t*>(src[b]) + nbytes[b] * next->first_flat,
-                            nbytes[b] * (size_t)E, hipMemcpyHostToDevice, next->copy));
-    }
-    if (next->done) MC_HIP(hipEventRecord(next->done, next->copy));
-  }
+  if (next && (rc = prefetch_launch("moe_experts_prefill", next, E)) != MC_OK) return rc;
   if (T == 0) return MC_OK;
   MC_REQUIRE(x_bf16 && ids && w && ws && y_bf16, "moe_experts_prefill: NULL pointer");
   return prefill_steps(x_bf16, ids, w, T, k, n_tok, E, layer_buf, nullptr, MC_PF_ALL, ws, nullptr, y_bf16, s);

@@ -1,0 +1,132 @@
+// moe_experts_prefill_act: the prefill MoE layer as grouped products on MXFP4 or bf16
+// activations ([jjl357] "4.1"-"4.3", "6.8").
+//
+// Steps on the compute stream, fixed grids, no host synchronisation: the token sort; for MXFP4
+// activations x quantised once per token; gate_up product of each expert's routes with the
+// SwiGLU (and the quantisation of h) in its epilogue, rows in sorted order; down product whose
+// epilogue multiplies by the gate and scatters each route to its own row of a [T*k][H] fp32
+// buffer (no atomics); the sum of each token's routes in route order, rounded once.
+#include "prefill.h"
+#include "product.h"
+
+namespace mc {
+
+static size_t align256(size_t v) { return (v + 255) & ~(size_t)255; }
+
+struct ActWs {
+  SortBuffers sort;
+  uint8_t *xq, *xqs;          // MXFP4 x: [T][H/2], [T][H/32]
+  uint8_t *h, *hs;            // sorted rows of h: bf16 [T*k][I], or MXFP4 codes and scales
+  float* yr;                  // [T*k][H]
+};
+
+static size_t ws_layout(int T, int k, int E, int H, int I, int act, ActWs* w, uint8_t* base) {
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* p = base + o;
+    o = align256(o + bytes);
+    return p;
+  };
+  const size_t nr = (size_t)T * k;
+  ActWs v{};
+  v.sort.counts = (int32_t*)take((size_t)E * 4);
+  v.sort.counts4 = (int32_t*)take((size_t)E * 16);
+  v.sort.offsets = (int32_t*)take((size_t)(E + 1) * 4);
+  v.sort.mtile_off = (int32_t*)take((size_t)(E + 1) * 4);
+  v.sort.perm = (int32_t*)take(nr * 4);
+  if (act == MC_MXFP4) {
+    v.xq = take((size_t)T * H / 2);
+    v.xqs = take((size_t)T * H / 32);
+    v.h = take(nr * I / 2);
+    v.hs = take(nr * I / 32);
+  } else {
+    v.h = take(nr * I * 2);
+  }
+  v.yr = (float*)take(nr * H * 4);
+  if (w) *w = v;
+  return o;
+}
+
+}  // namespace mc
+
+using namespace mc;
+
+extern "C" size_t moe_experts_prefill_act_ws_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I, int32_t act) {
+  if (T < 0 || k < 0 || E < 0 || H < 0 || I < 0 || (act != MC_BF16 && act != MC_MXFP4)) return 0;
+  return ws_layout(T, k, E, H, I, act, nullptr, nullptr);
+}
+
+extern "C" int moe_experts_prefill_act(const void* x_bf16, const int32_t* ids, const float* w, int32_t T, int32_t k,
+                                       const int32_t* n_tok, int32_t E, const mc_banks* buf, int32_t act, void* ws,
+                                       size_t ws_bytes, void* y_bf16, hipStream_t s, const mc_prefetch* next) {
+  clear_error();
+  const char* fn = "moe_experts_prefill_act";
+  int rc;
+  if ((rc = check_banks(buf, fn)) != MC_OK) return rc;
+  MC_REQUIRE(act == MC_BF16 || act == MC_MXFP4, "%s: activations of format %d", fn, act);
+  MC_REQUIRE(act == MC_BF16 || buf->fmt == MC_MXFP4, "%s: MXFP4 activations need MXFP4 experts", fn);
+  MC_REQUIRE(T >= 0 && k >= 1 && E >= 1 && E <= kP_MaxE && k <= E, "%s: T=%d k=%d E=%d", fn, T, k, E);
+  MC_REQUIRE((int64_t)T * k <= 0x7FFFFFFF, "%s: T=%d x k=%d routes are too many", fn, T, k);
+  MC_REQUIRE(buf->n >= E, "%s: layer buffer holds %lld < E=%d experts", fn, (long long)buf->n, E);
+  const int H = buf->H, I = buf->I;
+  MC_REQUIRE(I <= 0x3FFFFFFF, "%s: I=%d is too large", fn, I);
+  const size_t need = moe_experts_prefill_act_ws_bytes(T, k, E, H, I, act);
+  MC_REQUIRE(T == 0 || ws_bytes >= need, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
+  MC_REQUIRE(((uintptr_t)x_bf16 | (uintptr_t)ws | (uintptr_t)y_bf16) % 16 == 0, "%s: x, ws and y must be 16-byte aligned",
+             fn);
+  MC_REQUIRE(T == 0 || (x_bf16 && ids && w && ws && y_bf16), "%s: NULL pointer", fn);
+  if (next && (rc = prefetch_launch(fn, next, E)) != MC_OK) return rc;
+  if (T == 0) return MC_OK;
+
+  ActWs v{};
+  ws_layout(T, k, E, H, I, act, &v, static_cast<uint8_t*>(ws));
+  if ((rc = sort_routes_launch(ids, T, k, n_tok, E, v.sort, s)) != MC_OK) return rc;
+  if (act == MC_MXFP4 && (rc = mc_mxfp4_quantize(x_bf16, MC_BF16, T, H, H, v.xq, v.xqs, s)) != MC_OK) return rc;
+
+  ProductArgs p{};
+  p.E = E;
+  p.n = buf->n;
+  p.M = T * k;
+  p.offsets = v.sort.offsets;
+  p.perm = v.sort.perm;
+  p.x_fmt = act;
+  p.w_fmt = buf->fmt;
+  // h = silu(x W_gate^T) * (x W_up^T), rows in sorted order
+  p.x = act == MC_MXFP4 ? v.xq : static_cast<const uint8_t*>(x_bf16);
+  p.xs = v.xqs;
+  p.ldx = H;
+  p.x_rows = T;
+  p.x_div = k;
+  p.x_perm = 1;
+  p.w = static_cast<const uint8_t*>(buf->gate_up);
+  p.ws = static_cast<const uint8_t*>(buf->gate_up_scale);
+  p.N = 2 * I;
+  p.K = H;
+  p.swiglu = 1;
+  p.y = v.h;
+  p.ys = v.hs;
+  p.y_fmt = act;
+  p.ldy = I;
+  p.y_rows = T * k;
+  if ((rc = launch_product(p, s)) != MC_OK) return rc;
+  // the gated route outputs
+  p.x = v.h;
+  p.xs = v.hs;
+  p.ldx = I;
+  p.x_rows = T * k;
+  p.w = static_cast<const uint8_t*>(buf->down);
+  p.ws = static_cast<const uint8_t*>(buf->down_scale);
+  p.N = H;
+  p.K = I;
+  p.swiglu = 0;
+  p.x_perm = 0;
+  p.y = reinterpret_cast<uint8_t*>(v.yr);
+  p.ys = nullptr;
+  p.y_fmt = MC_F32;
+  p.ldy = H;
+  p.y_perm = 1;
+  p.gate = w;
+  p.n_gate = T * k;
+  if ((rc = launch_product(p, s)) != MC_OK) return rc;
+  return combine_launch(ids, T, k, E, H, n_tok, v.yr, static_cast<uint16_t*>(y_bf16), s);
+}

@@ -433,6 +433,124 @@ int moe_experts_prefill_part(const void* x_bf16, const int32_t* ids, const float
 int moe_experts_prefill_status(const void* ws, hipStream_t s, uint32_t* status);
 
 /* ------------------------------------------------------------------------- */
+/* MXFP4 quantisation and products                                           */
+/* ------------------------------------------------------------------------- */
+
+/* Element types of the calls below, beside mc_wfmt's MC_BF16 and MC_MXFP4. */
+enum { MC_F32 = 2, MC_F16 = 3 };
+
+/*
+ * Rows to MXFP4, the format of the expert banks (mc_banks): what turns a bf16, fp16 or
+ * fp32 checkpoint into banks, and activations into an operand of the products below
+ * ([jjl357] "6.9", "8.4": the experts are kept and consumed in MXFP4 blocks).
+ * Every 32 consecutive elements of a row share a scale 2^e, e = floor(log2 max|v|) - 2
+ * clamped to [-127, 127] (OCP MX v1.0; 0 if the block is all zeros: byte 0), and each
+ * element becomes the e2m1 value nearest to v / 2^e, ties to the even code, magnitudes
+ * over 6 to 6.  A block that holds an infinity or a NaN is written as e8m0's NaN (byte
+ * 255, codes 0).
+ *   src    device, `type` MC_BF16, MC_F16 or MC_F32, [rows] rows of `cols` elements that
+ *          start ld elements apart (ld >= cols, ld % 8 == 0); 16-byte aligned
+ *   codes  device u8 [rows][cols/2] out, 16-byte aligned; scales device u8 [rows][cols/32]
+ *          out, any alignment
+ * cols % 32 == 0, rows >= 0.  No host synchronisation; capturable.
+ */
+int mc_mxfp4_quantize(const void* src, int32_t type, int64_t rows, int64_t cols, int64_t ld,
+                      void* codes, void* scales, hipStream_t s);
+
+/*
+ * The values of MXFP4 rows: dst = e2m1(code) * 2^(X - 127), rounded once to `type` (bf16 and
+ * fp32 hold every value down to their subnormals' last bit; fp16 overflows to infinity and
+ * rounds below 2^-24).  X = 255 gives NaN.  Layout and limits as mc_mxfp4_quantize, dst
+ * rows ld elements apart; the elements between a row's end and the next row are left as
+ * they are.
+ */
+int mc_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t cols,
+                        void* dst, int32_t type, int64_t ld, hipStream_t s);
+
+/*
+ * Product with an MXFP4 matrix: y[m][n] = sum_k x[m][k] * w[n][k].
+ *   x    device, x_fmt MC_BF16: [M] rows ldx elements apart (ldx >= K, ldx % 8 == 0), or
+ *        MC_MXFP4: codes u8 [M][K/2] with x_scale u8 [M][K/32] (ldx unused)
+ *   w, w_scale  device MXFP4 [N][K/2], [N][K/32]
+ *   y    device, y_fmt MC_BF16 or MC_F32, [M] rows ldy elements apart (ldy >= N)
+ * x, w and y are 16-byte aligned, scales have any alignment.  Products are exact and summed
+ * in fp32 (the order depends on the sizes only), each result is rounded once.  K % 32 == 0,
+ * K >= 32; M = 0 or N = 0 enqueues nothing.  A NaN scale makes the results that read it NaN.
+ * y may not overlap an input.
+ */
+int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt, int64_t ldx, const void* w,
+                    const void* w_scale, int32_t M, int32_t N, int32_t K, void* y, int32_t y_fmt,
+                    int64_t ldy, hipStream_t s);
+
+/*
+ * Matrix products grouped by expert, with any number of rows per expert ([jjl357] "6.8":
+ * grouped GPU execution).  Sorted row i belongs to the group e with offsets[e] <= i <
+ * offsets[e+1]:
+ *   r     = perm ? perm[i] : i                      (a route, where perm is the token sort's)
+ *   v[n]  = sum_k x[x_perm ? r / x_div : i][k] * w[entry][n][k],
+ *           entry = entry_of ? entry_of[e] : e
+ *   v     = swiglu ? silu(v[0 .. N/2)) * v[N/2 .. N) : v
+ *   y[y_perm ? r : i] = (gate ? gate[r] : 1) * v
+ * With mc_prefill_sort_routes' offsets and perm, x_perm = 1 and x_div = k, row i is a route of
+ * expert e and x the tokens' activations; y_perm = 1 scatters results back to the routes.
+ *   x, w, y  as in mc_mxfp4_matmul, w being n matrices [N][K] one behind the other (the
+ *            gate_up or down bank of an mc_banks); formats (x, w): (bf16, bf16), (bf16, MXFP4),
+ *            (MXFP4, MXFP4).  y_fmt MC_MXFP4 writes the rows quantised (mc_mxfp4_quantize of
+ *            the fp32 results): codes to y, scales to y_scale, for an output width
+ *            divisible by 32.
+ *   offsets  device int32 [E+1], not descending; entries are clamped to [0, M]
+ *   perm     device int32 [M] or NULL; entry_of device int32 [E] or NULL
+ *   gate     device fp32 [n_gate], indexed by r, or NULL
+ * Rows of y that no sorted row maps to are left as they are: rows outside
+ * [offsets[0], offsets[E]), and rows of groups whose entry is outside [0, n) (-1: not in this
+ * part).  A row with negative r, whose row of x, row of y or gate is outside [0, x_rows),
+ * [0, y_rows) or [0, n_gate), is skipped.  With y_perm the entries of perm in use have to differ.
+ * K % 32 == 0, K >= 32, 1 <= E <= 1024, N even with swiglu.  Fixed summation order (by the
+ * sizes only): results are run-to-run identical.  No workspace, no host synchronisation;
+ * capturable, and the group sizes may change between replays.
+ */
+typedef struct {
+  int32_t x_fmt, w_fmt, y_fmt;
+  int32_t swiglu;
+  int32_t E, M, N, K;           /* groups, sorted rows, rows and columns of one matrix of w */
+  int32_t x_rows, x_div;        /* rows of x; x_div >= 1 */
+  int32_t y_rows;               /* rows of y */
+  int32_t x_perm, y_perm;       /* 0 or 1; 1 needs perm */
+  int32_t n_gate;               /* gates (unused without) */
+  int64_t ldx, ldy;             /* elements between rows of x and y */
+  int64_t n;                    /* matrices in w */
+  const void *x, *x_scale;
+  const void *w, *w_scale;
+  void *y, *y_scale;
+  const int32_t *offsets, *perm, *entry_of;
+  const float* gate;
+} mc_grouped;
+
+int mc_grouped_matmul(const mc_grouped* g, hipStream_t s);
+
+/*
+ * Prefill MoE layer with a choice of activations, for bf16 experts too (moe_experts_prefill
+ * is MXFP4 experts on bf16 activations):
+ *   y[t] = bf16_rne( sum_j w[t][j] * W_down q(silu(W_gate q(x[t])) * (W_up q(x[t]))) )
+ * for t < *n_tok (else 0) over the valid routes, q rounding to the activations' format:
+ *   act MC_MXFP4  MXFP4 experts; x and h are quantised (mc_mxfp4_quantize's rule) and the
+ *                 products run on the matrix cores' fp4 instructions, four times the bf16
+ *                 rate; the quantisation costs about 0.1-0.15 relative to bf16 activations
+ *   act MC_BF16   MXFP4 or bf16 experts; x is bf16 already, h is rounded to bf16
+ * Sort, gate_up product with SwiGLU (and the quantisation of h) in its epilogue, down product
+ * with the gates, and a fixed-order sum of each token's routes: results are run-to-run
+ * identical.  Sums are fp32.  Any T >= 0, E <= 1024, k <= E; H and I multiples of 64.
+ *   ws  device workspace of moe_experts_prefill_act_ws_bytes bytes, 16-byte aligned, one per
+ *       call in flight; next: as in moe_experts_prefill (layer_buf's format and shape).
+ */
+size_t moe_experts_prefill_act_ws_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I,
+                                        int32_t act);
+int moe_experts_prefill_act(const void* x_bf16, const int32_t* ids, const float* w, int32_t T,
+                            int32_t k, const int32_t* n_tok, int32_t E, const mc_banks* layer_buf,
+                            int32_t act, void* ws, size_t ws_bytes, void* y_bf16, hipStream_t s,
+                            const mc_prefetch* next);
+
+/* ------------------------------------------------------------------------- */
 /* Hybrid split / merge and the host branch                                  */
 /* ------------------------------------------------------------------------- */
 

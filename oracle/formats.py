@@ -80,3 +80,29 @@ def expert_matrices(banks: dict, idx: int, fmt: str, H: int, I: int):
     else:
         raise ValueError(fmt)
     return gu[:I], gu[I:], dn
+
+
+def encode_mxfp4(v: np.ndarray):
+    """Rows -> MXFP4: (codes uint8 [..., C/2], scales uint8 [..., C/32]) of float values [..., C].
+
+    Per block of 32: e = floor(log2 max|v|) - 2 clamped to [-127, 127], then the nearest of the
+    eight e2m1 magnitudes to |v| / 2^e (ties to the even code, anything over 6 to 6), found by
+    comparing the distances to all eight.  A block of zeros takes the scale byte 0; a block with an
+    infinity or a NaN the byte 255 and codes 0.
+    """
+    v = np.asarray(v, dtype=np.float64)
+    b = v.reshape(v.shape[:-1] + (v.shape[-1] // 32, 32))
+    bad = ~np.isfinite(b).all(axis=-1)
+    b = np.where(bad[..., None], 0.0, b)
+    amax = np.abs(b).max(axis=-1)
+    # frexp: amax = m * 2^x with m in [1/2, 1), so floor(log2 amax) = x - 1
+    e = np.where(amax > 0, np.frexp(amax)[1] - 1 - 2, -127)
+    e = np.clip(e, -127, 127)
+    u = np.minimum(np.abs(np.ldexp(b, -e[..., None])), 6.0)
+    dist = np.abs(u[..., None] - _E2M1[:8])
+    # of two equally near codes the even one: distances are exact, so order by (distance, odd)
+    code = np.lexsort((np.broadcast_to(np.arange(8) & 1, dist.shape), dist), axis=-1)[..., 0]
+    code = np.where(np.signbit(b), code | 8, code).astype(np.uint8).reshape(v.shape)
+    scales = np.where(bad, 255, e + 127).astype(np.uint8)
+    code = np.where(np.repeat(bad, 32, axis=-1), 0, code).astype(np.uint8)
+    return (code[..., 0::2] | (code[..., 1::2] << 4)).astype(np.uint8), scales
