@@ -29,21 +29,52 @@ __device__ __forceinline__ int group_rows(const ProductArgs& a, int e, int* lo) 
   return en >= 0 && en < a.n ? max(t - b, 0) : 0;
 }
 
-// Tile L of the call: row tiles of BM rows group by group, a group's tiles column block by
-// column block (consecutive tiles share the weights).  Every wave runs the search by itself:
-// lane l looks at group 64 c + l, a prefix sum over the lanes gives each group's first tile.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const ProductArgs& a, int L, int n_nb, Tile* t) {
+// Consecutive tiles L on the same XCD: workgroup b runs on XCD b % 8; `total` tiles are dealt
+// out in eight runs whose lengths differ by at most one.
+__device__ __forceinline__ int xcd_order(int b, int total) {
+  const int x = b & 7, q = total >> 3, r = total & 7;
+  return x * q + min(x, r) + (b >> 3);
+}
+
+// Place of tile p of a group with m row tiles and n_nb column blocks: bands of 8 row tiles,
+// column block by column block within a band, so that tiles running at the same time share
+// both the weights of a few column blocks and the rows of a few row tiles.
+__device__ __forceinline__ void tile_place(int p, int m, int n_nb, int* mt, int* nb) {
+  const int band = p / (8 * n_nb), in = p - band * 8 * n_nb;
+  const int h = min(8, m - band * 8);              // row tiles of this band
+  *nb = in / h;
+  *mt = band * 8 + in - *nb * h;
+}
+
+// Tile of workgroup `b` (XCD: dealt out by xcd_order): row tiles of BM rows, group by group.
+// Every wave runs the search by itself: lane l looks at group 64 c + l, a prefix sum over the
+// lanes gives each group's first tile.
+template <int BM, bool XCD>
+__device__ __forceinline__ bool find_tile(const ProductArgs& a, int b, int n_nb, Tile* t) {
   if (!a.offsets) {
     const int m = (a.M + BM - 1) / BM;
-    if (L >= m * n_nb) return false;
+    if (b >= m * n_nb) return false;
+    int mt;
+    tile_place(XCD ? xcd_order(b, m * n_nb) : b, m, n_nb, &mt, &t->nb);
     t->entry = 0;
-    t->nb = L / m;
-    t->row0 = (L - t->nb * m) * BM;
+    t->row0 = mt * BM;
     t->nrows = min(BM, a.M - t->row0);
     return true;
   }
   const int lane = threadIdx.x & 63;
+  int L = b;
+  if (XCD) {
+    int m = 0;
+    for (int e = lane; e < a.E; e += 64) {
+      int lo;
+      m += (group_rows(a, e, &lo) + BM - 1) / BM;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m += __shfl_xor(m, o, 64);
+    const int total = __builtin_amdgcn_readfirstlane(m) * n_nb;
+    if (b >= total) return false;
+    L = xcd_order(b, total);
+  }
   const int j = L / n_nb;
   int before = 0;
   for (int base = 0; base < a.E; base += 64) {
@@ -60,17 +91,17 @@ __device__ __forceinline__ bool find_tile(const ProductArgs& a, int L, int n_nb,
     const uint64_t past = __ballot(before + incl > j);
     if (past) {
       const int src = __ffsll((unsigned long long)past) - 1;
-      const int first = before + __shfl(incl - m, src, 64);
-      const int me = __shfl(m, src, 64), lo_e = __shfl(lo, src, 64), rows_e = __shfl(rows, src, 64);
-      const int Lp = L - first * n_nb;
-      t->nb = Lp / me;
-      const int mt = Lp - t->nb * me;
+      const int first = before + __builtin_amdgcn_readlane(incl - m, src);
+      const int me = __builtin_amdgcn_readlane(m, src), lo_e = __builtin_amdgcn_readlane(lo, src);
+      const int rows_e = __builtin_amdgcn_readlane(rows, src);
+      int mt;
+      tile_place(L - first * n_nb, me, n_nb, &mt, &t->nb);
       t->row0 = lo_e + mt * BM;
       t->nrows = min(BM, rows_e - mt * BM);
       t->entry = a.entry_of ? a.entry_of[base + src] : base + src;
       return true;
     }
-    before += __shfl(incl, 63, 64);
+    before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -108,48 +139,60 @@ __device__ __forceinline__ void store4(const ProductArgs& a, int64_t row, int co
   }
 }
 
-// Output of NF 16-column fragments of one 16-row fragment: fragment f holds columns
-// col0 + 16 f + 4 (lane / 16) + i of row i_row (the lane's: lane % 16 of the fragment).
-// `on` is false for lanes past the tile's rows (they stay for the lane exchanges).
-template <int NF>
-__device__ __forceinline__ void store_row(const ProductArgs& a, int i_row, bool on, int col0, int n_out,
-                                          const f32x4_t* v) {
-  const int lane = threadIdx.x & 63, g = lane >> 4;
-  const int r = a.perm ? a.perm[i_row] : i_row;
-  const int64_t yr = a.y_perm ? r : i_row;
-  on = on && r >= 0 && x_row(a, i_row, r) >= 0 && yr < a.y_rows && (!a.gate || r < a.n_gate);
-  const float s = a.gate && on ? a.gate[r] : 1.0f;
-  if (a.y_fmt == MC_MXFP4) {
-    // two neighbouring fragments are one block of 32 columns: its 8 lane quarters of four
-    // columns meet by lane exchanges over lane bits 4 and 5
-#pragma unroll
-    for (int f = 0; f + 1 < NF; f += 2) {
-      float o[8];
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i] = s * v[f + i / 4][i % 4];
-        m = max(m, abs_bits(o[i]));
-      }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
-      const uint32_t X = block_exponent(m);
-      const uint32_t c = fp4x8_codes(o, X);
-      const int col = col0 + 16 * f;
-      if (on && col < n_out) {
-        uint8_t* p = a.y + yr * (int64_t)(n_out / 2) + (col >> 1) + 2 * g;
-        *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
-        *reinterpret_cast<uint16_t*>(p + 8) = (uint16_t)(c >> 16);
-        if (g == 0) a.ys[yr * (int64_t)(n_out / 32) + (col >> 5)] = (uint8_t)X;
-      }
-    }
-  } else if (on) {
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const int col = col0 + 16 * f + 4 * g;
-      if (col < n_out) store4(a, yr, col, n_out, a.gate ? s * v[f] : v[f]);
-    }
+// Where sorted row i goes: its row of y (-1: nowhere) and its gate.
+struct RowOut {
+  int64_t y;
+  float gate;
+};
+
+__device__ __forceinline__ RowOut row_out(const ProductArgs& a, int i, bool on) {
+  const int r = a.perm ? a.perm[i] : i;
+  const int yr = a.y_perm ? r : i;
+  on = on && r >= 0 && x_row(a, i, r) >= 0 && yr < a.y_rows && (!a.gate || r < a.n_gate);
+  return RowOut{on ? yr : -1, a.gate && on ? a.gate[r] : 1.0f};
+}
+
+// Two 16-column fragments v (32 neighbouring columns from col0) of one 16-row fragment: v[f][i] is
+// column col0 + 16 f + 4 (lane / 16) + i of the lane's row (lane % 16 of the fragment).
+__device__ __forceinline__ void store_pair(const ProductArgs& a, const RowOut& o, int col0, int n_out, f32x4_t v0,
+                                           f32x4_t v1) {
+  const int g = (threadIdx.x & 63) >> 4;
+  if (a.gate) {
+    v0 *= o.gate;
+    v1 *= o.gate;
   }
+  if (a.y_fmt == MC_MXFP4) {
+    // the block's 8 quarters of four columns meet by lane exchanges over lane bits 4 and 5
+    float e[8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      e[i] = v0[i];
+      e[4 + i] = v1[i];
+      m = max(m, max(abs_bits(v0[i]), abs_bits(v1[i])));
+    }
+    m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
+    m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
+    const uint32_t X = block_exponent(m);
+    const uint32_t c = fp4x8_codes(e, X);
+    if (o.y >= 0 && col0 < n_out) {
+      uint8_t* p = a.y + o.y * (int64_t)(n_out / 2) + (col0 >> 1) + 2 * g;
+      *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
+      *reinterpret_cast<uint16_t*>(p + 8) = (uint16_t)(c >> 16);
+      if (g == 0) a.ys[o.y * (int64_t)(n_out / 32) + (col0 >> 5)] = (uint8_t)X;
+    }
+  } else if (o.y >= 0) {
+    const int col = col0 + 4 * g;
+    if (col < n_out) store4(a, o.y, col, n_out, v0);
+    if (col + 16 < n_out) store4(a, o.y, col + 16, n_out, v1);
+  }
+}
+
+__device__ __forceinline__ f32x4_t swiglu4(const f32x4_t& g, const f32x4_t& u) {
+  f32x4_t h;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i];
+  return h;
 }
 
 // ---------------------------------------------------------------- operands from memory
@@ -177,7 +220,7 @@ template <int XF, int WF>
 __global__ void __launch_bounds__(256)
 product_kernel(ProductArgs a, int n_nb) {
   Tile t;
-  if (!find_tile<kBM>(a, blockIdx.x, n_nb, &t)) return;
+  if (!find_tile<kBM, false>(a, blockIdx.x, n_nb, &t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   if (wave * 16 >= t.nrows) return;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
@@ -239,15 +282,282 @@ product_kernel(ProductArgs a, int n_nb) {
       }
     }
   }
+  const RowOut o = row_out(a, i_row, m < t.nrows);
   if (a.swiglu) {
-    f32x4_t h[2];
-#pragma unroll
-    for (int f = 0; f < 2; ++f)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[f][i] = silu(acc[f][i]) * acc[f + 2][i];
-    store_row<2>(a, i_row, m < t.nrows, c0, n_out, h);
+    store_pair(a, o, c0, n_out, swiglu4(acc[0], acc[2]), swiglu4(acc[1], acc[3]));
   } else {
-    store_row<4>(a, i_row, m < t.nrows, c0, n_out, acc);
+    store_pair(a, o, c0, n_out, acc[0], acc[1]);
+    store_pair(a, o, c0 + 32, n_out, acc[2], acc[3]);
+  }
+}
+
+// ---------------------------------------------------------------- many rows
+//
+// 256 rows x 256 weight rows (SwiGLU: 128 gate and the matching 128 up rows) per workgroup of 8
+// waves, 2 along the rows x 4 along the weight rows: a wave multiplies MF 16-row fragments
+// (rows 32 f + 16 wm of the tile, so that a tile of fewer rows runs fewer fragments in every
+// wave alike) with 64 weight rows (32 at 32 wn of each half of the weight tile: with SwiGLU
+// the gate rows and their up rows).  K moves in stages of 64 bytes per row through a ring of
+// four LDS buffers (global_load_lds, no registers): stage s + 3 is requested when stage s
+// begins, one barrier per stage.  A row's four 16-byte chunks are stored at chunk
+// c ^ (row / 2 % 4), with which the operand reads run at the LDS's full rate (221 of
+// 256 B/clk measured, 120 without it).
+//
+// kBf16: bf16 x bf16, 32 elements per stage.  kFp4: MXFP4 x MXFP4, 128 elements per stage, the
+// four scale bytes of each row's stage in a small ring of their own.  kA16W4: bf16 rows in
+// stages of 32 elements; the weights' codes and scales come in every four stages (64 bytes per
+// row) into a ring of two and become bf16 when a wave reads its fragment.
+
+enum { kBf16 = 0, kA16W4 = 1, kFp4 = 2 };
+
+constexpr int kWideThreads = 512, kWideBM = 256, kWideBN = 256;
+constexpr int kRing = 4;
+constexpr int kTileBytes = 256 * 64;              // one operand's tile of a stage
+
+template <int VM>
+__device__ __forceinline__ void wait_stage() {
+  // at most VM loads outstanding, every LDS access done, then the workgroup's barrier
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+typedef __attribute__((address_space(3))) void* lds_ptr;
+
+// 16 (4) bytes per lane from src into LDS at dst + 16 (4) lane, dst the same for the wave.  Written
+// as an instruction with no register result: the compiler's builtin makes every later LDS read
+// wait for all such loads, those for other ring buffers among them.  The reader's wait is
+// wait_stage's; the compiler's own waits for other loads count these as unknown older or newer
+// ones, which can only make them longer.
+__device__ __forceinline__ void load_lds16(const uint8_t* src, void* dst) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(const uint8_t* src, void* dst) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)dst);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+}
+
+// Four scale bytes of blocks b .. b + 3 of a row of n blocks, at any alignment (blocks past the
+// last count as 2^0).
+__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int b, int n) {
+  uint32_t v = 0x7F7F7F7Fu;
+  if (b + 4 <= n) {
+    __builtin_memcpy(&v, row + b, 4);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (b + i < n) v = (v & ~(0xFFu << (8 * i))) | ((uint32_t)row[b + i] << (8 * i));
+  }
+  return v;
+}
+
+struct WideLds {
+  uint8_t x[kRing][kTileBytes];
+  uint8_t w[kRing][kTileBytes];
+  uint32_t s[kRing][512];                         // scales: weight rows, then rows (MXFP4)
+};
+struct WideLdsBf16 {
+  uint8_t x[kRing][kTileBytes];
+  uint8_t w[kRing][kTileBytes];
+};
+struct WideLdsA16 {
+  uint8_t x[kRing][kTileBytes];
+  uint8_t w[2][kTileBytes];
+  uint32_t s[2][256];
+};
+template <int MODE> struct WideLdsOf { typedef WideLds type; };
+template <> struct WideLdsOf<kBf16> { typedef WideLdsBf16 type; };
+template <> struct WideLdsOf<kA16W4> { typedef WideLdsA16 type; };
+
+// SDMA: the scales of a row start at a multiple of four bytes and K is a multiple of 128, so they
+// go straight into LDS like the operands; otherwise they pass through a register, whose wait
+// also drains the loads on their way.
+template <int MODE, bool SDMA, int MF>
+__device__ __forceinline__ void wide_tile(const ProductArgs& a, const Tile& t, typename WideLdsOf<MODE>::type& lds) {
+  constexpr int XQ = MF > 4 ? 2 : 1;              // x loads per thread and stage: 128 rows each
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+  const int wm = wave & 1, wn = wave >> 1;
+  const int n_out = a.swiglu ? a.N / 2 : a.N;
+  const int c0 = t.nb * (a.swiglu ? kWideBN / 2 : kWideBN);
+  const int64_t K = a.K;
+  const int64_t wrow_b = MODE == kBf16 ? 2 * K : K / 2, xrow_b = MODE == kFp4 ? K / 2 : 2 * a.ldx;
+  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;   // bytes of a row in use
+  const int stages = (xb + 63) / 64;
+
+  // this thread's 16 bytes of a stage: rows tid / 4 and 128 + tid / 4, logical chunk ch
+  const int ch = (tid & 3) ^ ((tid >> 3) & 3);
+  const uint8_t *wp[2], *xp[2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int row = a.swiglu ? min(c0 + (tid >> 2), n_out - 1) + q * n_out : min(c0 + q * 128 + (tid >> 2), n_out - 1);
+    wp[q] = a.w + ((int64_t)t.entry * a.N + row) * wrow_b + ch * 16;
+    const int i = t.row0 + min(q * 128 + (tid >> 2), t.nrows - 1);
+    xp[q] = a.x + (int64_t)max(x_row(a, i, a.perm ? a.perm[i] : i), 0) * xrow_b + ch * 16;
+  }
+  const uint8_t* sp = nullptr;                    // scales of weight row tid, and of row tid - 256
+  if (MODE != kBf16) {
+    if (tid < 256) {
+      const int r = tid & 127, q = tid >> 7;
+      const int row = a.swiglu ? min(c0 + r, n_out - 1) + q * n_out : min(c0 + tid, n_out - 1);
+      sp = a.ws + ((int64_t)t.entry * a.N + row) * (K / 32);
+    } else if (MODE == kFp4) {
+      const int i = t.row0 + min(tid - 256, t.nrows - 1);
+      sp = a.xs + (int64_t)max(x_row(a, i, a.perm ? a.perm[i] : i), 0) * (K / 32);
+    }
+  }
+  const int nblk = a.K / 32;
+  uint32_t sc = 0;
+  // 64 bytes of every weight row and the scales of their blocks: stage s (kA16W4: four stages)
+  auto request_w = [&](int s) {
+    const int b = MODE == kA16W4 ? s & 1 : s & (kRing - 1);
+    // a chunk past the row's end (only in the last stage) re-reads the row's first bytes
+    const int64_t off = s * 64 + ch * 16 < wb ? (int64_t)s * 64 : -(int64_t)(ch * 16);
+    if constexpr (MODE != kBf16) {
+      if (MODE == kFp4 || wave < 4) {
+        if (SDMA) load_lds4(sp + s * 4, &lds.s[b][wave * 64]);
+        else sc = load_scales(sp, s * 4, nblk);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q) load_lds16(wp[q] + off, &lds.w[b][q * 8192 + wave * 1024]);
+  };
+  auto request_x = [&](int s) {
+    const int b = s & (kRing - 1);
+    const int64_t off = s * 64 + ch * 16 < xb ? (int64_t)s * 64 : -(int64_t)(ch * 16);
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) load_lds16(xp[q] + off, &lds.x[b][q * 8192 + wave * 1024]);
+  };
+  auto put_scales = [&](int s) {
+    if constexpr (MODE != kBf16 && !SDMA) {
+      if (MODE == kFp4 || wave < 4) lds.s[MODE == kA16W4 ? s & 1 : s & (kRing - 1)][tid] = sc;
+    }
+  };
+
+  f32x4_t acc[4][MF];
+#pragma unroll
+  for (int f = 0; f < 4; ++f)
+#pragma unroll
+    for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+
+  const int swz = (l16 >> 1) & 3;
+  const int frag = l16 * 64 + ((g ^ swz) << 4);
+  const int xfrag = wm * 16 * 64 + frag;
+  auto compute = [&](int s) {
+    const int b = s & (kRing - 1);
+    u32x4_t w[4];
+    uint32_t sw[4];
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      const int row = (f >> 1) * 128 + (f & 1) * 16 + wn * 32;
+      if constexpr (MODE == kA16W4) {
+        // element 8 g of block s of the row: a dword of its 16-byte chunk
+        const int c = (s >> 2) & 1, j = s & 3;
+        const uint32_t code =
+            *reinterpret_cast<const uint32_t*>(&lds.w[c][(row + l16) * 64 + ((j ^ swz) << 4) + g * 4]);
+        const uint32_t X = reinterpret_cast<const uint8_t*>(lds.s[c])[(row + l16) * 4 + j];
+        w[f] = __builtin_bit_cast(u32x4_t, fp4x8_bf16(code, e8m0_or_nan(X)));
+      } else {
+        w[f] = *reinterpret_cast<const u32x4_t*>(&lds.w[b][row * 64 + frag]);
+        if constexpr (MODE == kFp4) sw[f] = lds.s[b][row + l16] >> (8 * g);
+      }
+    }
+#pragma unroll
+    for (int m = 0; m < MF; ++m) {
+      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(&lds.x[b][xfrag + m * 32 * 64]);
+      if constexpr (MODE == kFp4) {
+        const uint32_t sx = lds.s[b][256 + m * 32 + wm * 16 + l16] >> (8 * g);
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f][m] = mfma_fp4(w[f], sw[f], x, sx, acc[f][m]);
+      } else {
+#pragma unroll
+        for (int f = 0; f < 4; ++f) acc[f][m] = mfma_bf16(w[f], x, acc[f][m]);
+      }
+    }
+  };
+
+  if (MODE == kA16W4) {
+    request_w(0);
+    put_scales(0);
+  }
+  for (int s = 0; s < kRing - 1 && s < stages; ++s) {
+    if (MODE != kA16W4) {
+      request_w(s);
+      put_scales(s);
+    }
+    request_x(s);
+  }
+  int s = 0;
+  for (; s + kRing - 1 < stages; ++s) {
+    // stage s is in; s + 1 and s + 2 (and with s % 4 = 1, 2 the weights of the next four stages,
+    // requested with or after stage s + 1) may be on their way
+    if (MODE != kA16W4) wait_stage<2 * (2 + XQ + (MODE == kFp4 && SDMA))>();
+    else if (((s - 1) & 3) < 2) wait_stage<2 * XQ + 2>();
+    else wait_stage<2 * XQ>();
+    if (MODE != kA16W4) request_w(s + kRing - 1);
+    else if ((s & 3) == 0 && (s + 4) < stages) request_w((s >> 2) + 1);
+    request_x(s + kRing - 1);
+    compute(s);
+    if (MODE != kA16W4) put_scales(s + kRing - 1);
+    else if ((s & 3) == 0 && (s + 4) < stages) put_scales((s >> 2) + 1);
+  }
+  for (; s < stages; ++s) {
+    if (MODE == kFp4 && !SDMA && s + 1 == stages && (xb & 63)) {
+      // the last stage's chunks past the row's end count as zeros: of one operand, since every
+      // e2m1 code is finite
+      __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+      asm volatile("" ::: "memory");
+      if (s * 64 + ch * 16 >= wb) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<u32x4_t*>(&lds.w[s & (kRing - 1)][q * 8192 + tid * 16]) = u32x4_t{0, 0, 0, 0};
+      }
+    }
+    wait_stage<0>();
+    compute(s);
+  }
+
+  RowOut o[MF];
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    const int r = m * 32 + wm * 16 + l16;
+    o[m] = row_out(a, t.row0 + min(r, t.nrows - 1), r < t.nrows);
+  }
+#pragma unroll
+  for (int m = 0; m < MF; ++m) {
+    if (a.swiglu) {
+      store_pair(a, o[m], c0 + wn * 32, n_out, swiglu4(acc[0][m], acc[2][m]), swiglu4(acc[1][m], acc[3][m]));
+    } else {
+      store_pair(a, o[m], c0 + wn * 32, n_out, acc[0][m], acc[1][m]);
+      store_pair(a, o[m], c0 + 128 + wn * 32, n_out, acc[2][m], acc[3][m]);
+    }
+  }
+}
+
+template <int MODE, bool SDMA>
+__global__ void __launch_bounds__(kWideThreads, 2)
+product_wide_kernel(ProductArgs a, int n_nb) {
+  __shared__ __attribute__((aligned(16))) typename WideLdsOf<MODE>::type lds;
+  Tile t;
+  if (!find_tile<kWideBM, true>(a, blockIdx.x, n_nb, &t)) return;
+  // 32-row steps of the tile, the same for the whole workgroup
+  const int steps = (t.nrows + 31) >> 5;
+  if constexpr (SDMA) {
+    switch (steps) {
+      case 1: wide_tile<MODE, SDMA, 1>(a, t, lds); break;
+      case 2: wide_tile<MODE, SDMA, 2>(a, t, lds); break;
+      case 3: wide_tile<MODE, SDMA, 3>(a, t, lds); break;
+      case 4: wide_tile<MODE, SDMA, 4>(a, t, lds); break;
+      case 5: wide_tile<MODE, SDMA, 5>(a, t, lds); break;
+      case 6: wide_tile<MODE, SDMA, 6>(a, t, lds); break;
+      case 7: wide_tile<MODE, SDMA, 7>(a, t, lds); break;
+      default: wide_tile<MODE, SDMA, 8>(a, t, lds); break;
+    }
+  } else {
+    if (steps <= 2) wide_tile<MODE, SDMA, 2>(a, t, lds);
+    else if (steps <= 4) wide_tile<MODE, SDMA, 4>(a, t, lds);
+    else wide_tile<MODE, SDMA, 8>(a, t, lds);
   }
 }
 
@@ -291,15 +601,28 @@ int check_product(const char* fn, const ProductArgs& a) {
 
 int launch_product(const ProductArgs& a, hipStream_t s) {
   if (a.M == 0 || a.N == 0 || a.x_rows == 0 || a.y_rows == 0 || a.n == 0) return MC_OK;
-  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? kBN / 2 : kBN;
+  const bool wide = a.M > 32;
+  const int64_t bm = wide ? kWideBM : kBM, bn = wide ? kWideBN : kBN;
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? bn / 2 : bn;
   const int64_t n_nb = (n_out + cols - 1) / cols;
-  // sum over groups of ceil(rows / BM)
-  const int64_t mt = a.M / kBM + (a.offsets ? (a.E < a.M ? a.E : a.M) : 1);
+  // sum over groups of ceil(rows / bm)
+  const int64_t mt = a.offsets ? a.M / bm + (a.E < a.M ? a.E : a.M) : (a.M + bm - 1) / bm;
   MC_REQUIRE(mt * n_nb <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
-  const dim3 grid((unsigned)(mt * n_nb)), block(256);
-  if (a.x_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_MXFP4, MC_MXFP4>), grid, block, 0, s, a, (int)n_nb);
-  else if (a.w_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_BF16, MC_MXFP4>), grid, block, 0, s, a, (int)n_nb);
-  else hipLaunchKernelGGL((product_kernel<MC_BF16, MC_BF16>), grid, block, 0, s, a, (int)n_nb);
+  const dim3 grid((unsigned)(mt * n_nb)), block(wide ? kWideThreads : 256);
+  const int nb = (int)n_nb;
+  if (wide) {
+    const bool sdma = a.K % 128 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 4 == 0;
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, nb); };
+    if (a.w_fmt == MC_BF16) run(product_wide_kernel<kBf16, true>);
+    else if (a.x_fmt == MC_BF16 && sdma) run(product_wide_kernel<kA16W4, true>);
+    else if (a.x_fmt == MC_BF16) run(product_wide_kernel<kA16W4, false>);
+    else if (sdma) run(product_wide_kernel<kFp4, true>);
+    else run(product_wide_kernel<kFp4, false>);
+  } else {
+    if (a.x_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_MXFP4, MC_MXFP4>), grid, block, 0, s, a, nb);
+    else if (a.w_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_BF16, MC_MXFP4>), grid, block, 0, s, a, nb);
+    else hipLaunchKernelGGL((product_kernel<MC_BF16, MC_BF16>), grid, block, 0, s, a, nb);
+  }
   MC_LAUNCH_CHECK();
   return MC_OK;
 }
