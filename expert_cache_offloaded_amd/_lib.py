@@ -373,95 +373,120 @@ def moe_experts_prefill_part(x, ids, w, n_tok, E: int, part_buf: Banks, entry_of
 
 # ---------------------------------------------------------------- MXFP4 and grouped products
 
-def _types():
+_torch = None
+_type_ids = {}
+
+
+def _load_torch():
+    global _torch
     import torch
-    return {torch.bfloat16: MC_BF16, torch.int16: MC_BF16, torch.float32: MC_F32, torch.float16: MC_F16,
-            torch.uint8: MC_MXFP4}
-
-
-_type_ids = None
+    _torch = torch
+    _type_ids.update({torch.bfloat16: MC_BF16, torch.int16: MC_BF16, torch.float32: MC_F32,
+                      torch.float16: MC_F16, torch.uint8: MC_MXFP4})
 
 
 def _etype(t) -> int:
     """Element type of a tensor: bf16 values or their bits (int16), fp32, fp16, MXFP4 codes (uint8)."""
-    global _type_ids
-    if _type_ids is None:
-        _type_ids = _types()
-    try:
-        return _type_ids[t.dtype]
-    except KeyError:
-        raise ValueError("no element type for %s tensors" % t.dtype) from None
+    if _torch is None:
+        _load_torch()
+    e = _type_ids.get(t.dtype)
+    if e is None:
+        raise ValueError("no element type for %s tensors" % t.dtype)
+    return e
 
 
-def _device(fn: str, first, *rest):
-    """The tensors' GPU: all of them on one."""
-    d = first.device
-    if d.type != "cuda" or any(t is not None and t.device != d for t in rest):
+def _device(fn: str, first, *rest) -> int:
+    """Index of the GPU that all the tensors are on."""
+    d = first.get_device()
+    for t in rest:
+        if t is not None and t.get_device() != d:
+            d = -1
+    if d < 0:
         raise ValueError("%s: tensors must all be on one GPU" % fn)
     return d
 
 
-def _on(device, stream):
-    """(stream handle, context): the given stream, or the current one of the tensors' GPU, with that
-    GPU current while the call is made."""
-    import contextlib
-
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    ctx = contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-    return stream.cuda_stream, ctx
+def _call(name: str, device: int, stream, fn, *args) -> None:
+    """fn(*args, stream handle) with the tensors' GPU current, on the given stream or on that GPU's
+    current one."""
+    raw = _torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if device == _torch._C._cuda_getDevice():
+        rc = fn(*args, raw)
+    else:
+        with _torch.cuda.device(device):
+            rc = fn(*args, raw)
+    if rc != MC_OK:
+        raise McError(name, rc, last_error())
 
 
 def _rows(fn: str, what: str, t, cols: int, rows: Optional[int] = None) -> int:
     """Leading stride of a 2-D tensor of `cols` columns whose rows are contiguous."""
-    if t.dim() != 2 or t.shape[1] != cols or (rows is not None and t.shape[0] != rows):
-        raise ValueError("%s: %s has shape %s" % (fn, what, tuple(t.shape)))
-    if t.numel() and t.shape[1] > 1 and t.stride(1) != 1:
+    shape = t.shape
+    if len(shape) != 2 or shape[1] != cols or (rows is not None and shape[0] != rows):
+        raise ValueError("%s: %s has shape %s" % (fn, what, tuple(shape)))
+    if shape[0] <= 1:
+        if not t.is_contiguous() and cols > 1 and t.stride(1) != 1:
+            raise ValueError("%s: the rows of %s must be contiguous" % (fn, what))
+        return max(cols, 1)
+    ld, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError("%s: the rows of %s must be contiguous" % (fn, what))
-    return t.stride(0) if t.shape[0] > 1 else max(cols, 1)
+    return ld
 
 
 def _packed(fn: str, what: str, t, shape, dtype) -> None:
     """A contiguous tensor of the given shape and type."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError("%s: %s must be a contiguous %s tensor of shape %s, not %s %s"
                          % (fn, what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
 def _codes(fn: str, what: str, codes, scales) -> int:
     """Checks MXFP4 codes [..., C/2] with scales [..., C/32]; returns C."""
-    import torch
     if scales is None:
         raise ValueError("%s: MXFP4 %s needs its scales" % (fn, what))
-    C_ = 2 * codes.shape[-1]
-    _packed(fn, what, codes, codes.shape, torch.uint8)
-    _packed(fn, what + "'s scales", scales, tuple(codes.shape[:-1]) + (C_ // 32,), torch.uint8)
-    return C_
+    if _torch is None:
+        _load_torch()
+    u8 = _torch.uint8
+    shape = codes.shape
+    if (codes.dtype != u8 or scales.dtype != u8 or not codes.is_contiguous() or not scales.is_contiguous()
+            or scales.shape[:-1] != shape[:-1] or scales.shape[-1] * 16 != shape[-1]):
+        raise ValueError("%s: %s must be contiguous uint8 codes [..., C/2] with scales [..., C/32], not %s %s and %s %s"
+                         % (fn, what, codes.dtype, tuple(shape), scales.dtype, tuple(scales.shape)))
+    return 2 * shape[-1]
 
 
 def mxfp4_quantize(src, codes, scales, stream=None) -> None:
     """Rows of src (bf16, fp16 or fp32 [rows][cols]; rows may lie apart) to MXFP4 codes u8
     [rows][cols/2] and scales u8 [rows][cols/32]."""
-    cols = _codes("mxfp4_quantize", "codes", codes, scales)
-    ld = _rows("mxfp4_quantize", "src", src, cols, codes.shape[0])
-    d = _device("mxfp4_quantize", src, codes, scales)
-    st, ctx = _on(d, stream)
-    with ctx:
-        _check("mc_mxfp4_quantize", lib().mc_mxfp4_quantize(
-            _ptr(src), _etype(src), src.shape[0], cols, ld if src.shape[0] > 1 else (ld + 7) & ~7, _ptr(codes),
-            _ptr(scales), st))
+    fn = "mxfp4_quantize"
+    cols = _codes(fn, "codes", codes, scales)
+    rows = codes.shape[0]
+    ld = _rows(fn, "src", src, cols, rows)
+    _call("mc_mxfp4_quantize", _device(fn, src, codes, scales), stream, lib().mc_mxfp4_quantize, src.data_ptr(),
+          _etype(src), rows, cols, ld, codes.data_ptr(), scales.data_ptr())
 
 
 def mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
     """The values of MXFP4 rows, to dst (bf16, fp16 or fp32 [rows][cols]; rows may lie apart)."""
-    cols = _codes("mxfp4_dequantize", "codes", codes, scales)
-    ld = _rows("mxfp4_dequantize", "dst", dst, cols, codes.shape[0])
-    d = _device("mxfp4_dequantize", dst, codes, scales)
-    st, ctx = _on(d, stream)
-    with ctx:
-        _check("mc_mxfp4_dequantize", lib().mc_mxfp4_dequantize(
-            _ptr(codes), _ptr(scales), codes.shape[0], cols, _ptr(dst), _etype(dst), ld, st))
+    fn = "mxfp4_dequantize"
+    cols = _codes(fn, "codes", codes, scales)
+    rows = codes.shape[0]
+    ld = _rows(fn, "dst", dst, cols, rows)
+    _call("mc_mxfp4_dequantize", _device(fn, dst, codes, scales), stream, lib().mc_mxfp4_dequantize, codes.data_ptr(),
+          scales.data_ptr(), rows, cols, dst.data_ptr(), _etype(dst), ld)
+
+
+def _x_operand(fn: str, x, x_scale, K: int):
+    """(format, leading stride) of the rows x of a product over K columns."""
+    xf = _etype(x)
+    if xf == MC_MXFP4:
+        if _codes(fn, "x", x, x_scale) != K or x.dim() != 2:
+            raise ValueError("%s: x has shape %s, w has %d columns" % (fn, tuple(x.shape), K))
+        return xf, K
+    if x_scale is not None:
+        raise ValueError("%s: x_scale belongs to MXFP4 x" % fn)
+    return xf, _rows(fn, "x", x, K)
 
 
 def mxfp4_matmul(x, w, w_scale, y, x_scale=None, stream=None) -> None:
@@ -472,25 +497,11 @@ def mxfp4_matmul(x, w, w_scale, y, x_scale=None, stream=None) -> None:
     K = _codes(fn, "w", w, w_scale)
     if w.dim() != 2:
         raise ValueError("%s: w has shape %s" % (fn, tuple(w.shape)))
+    M, N = x.shape[0], w.shape[0]
     xf, ldx = _x_operand(fn, x, x_scale, K)
-    ldy = _rows(fn, "y", y, w.shape[0], x.shape[0])
-    d = _device(fn, x, w, w_scale, y, x_scale)
-    st, ctx = _on(d, stream)
-    with ctx:
-        _check("mc_mxfp4_matmul", lib().mc_mxfp4_matmul(
-            _ptr(x), _ptr(x_scale), xf, ldx, _ptr(w), _ptr(w_scale), x.shape[0], w.shape[0], K, _ptr(y),
-            _etype(y), ldy, st))
-
-
-def _x_operand(fn: str, x, x_scale, K: int):
-    xf = _etype(x)
-    if xf == MC_MXFP4:
-        if _codes(fn, "x", x, x_scale) != K or x.dim() != 2:
-            raise ValueError("%s: x has shape %s, w has %d columns" % (fn, tuple(x.shape), K))
-        return xf, K
-    if x_scale is not None:
-        raise ValueError("%s: x_scale belongs to MXFP4 x" % fn)
-    return xf, _rows(fn, "x", x, K)
+    ldy = _rows(fn, "y", y, N, M)
+    _call("mc_mxfp4_matmul", _device(fn, x, w, w_scale, y, x_scale), stream, lib().mc_mxfp4_matmul, x.data_ptr(),
+          _ptr(x_scale), xf, ldx, w.data_ptr(), w_scale.data_ptr(), M, N, K, y.data_ptr(), _etype(y), ldy)
 
 
 def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, swiglu: bool = False, perm=None,
@@ -504,14 +515,14 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
       y         bf16 or fp32, or MXFP4 codes u8 with y_scale; N columns (N / 2 with swiglu)
       perm      int32: the route of every sorted row (prefill_sort_routes); x rows are then gathered
                 from perm[i] / x_div (x_perm=False: from i), y rows scattered to perm[i] with y_perm
-      gate      fp32 by route (by row without perm; rows past its end are skipped); entry_of int32 [E], -1 = leave the group out
+      gate      fp32 by route (by row without perm; rows past its end are skipped); entry_of int32
+                [E], -1 = leave the group out
     Without perm the number of rows is y's; with it perm's."""
-    import torch
     fn = "grouped_matmul"
+    wf = _etype(w)
     if w.dim() != 3:
         raise ValueError("%s: w has shape %s" % (fn, tuple(w.shape)))
-    wf = _etype(w)
-    K = w.shape[2]
+    n, N, K = w.shape
     if wf == MC_MXFP4:
         K = _codes(fn, "w", w, w_scale)
     elif w_scale is not None:
@@ -519,7 +530,7 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
     elif not w.is_contiguous():
         raise ValueError("%s: w must be contiguous" % fn)
     xf, ldx = _x_operand(fn, x, x_scale, K)
-    n_out = w.shape[1] // 2 if swiglu else w.shape[1]
+    n_out = N // 2 if swiglu else N
     yf = _etype(y)
     ldy = 0
     if yf == MC_MXFP4:
@@ -529,25 +540,25 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
         raise ValueError("%s: y_scale belongs to MXFP4 y" % fn)
     else:
         ldy = _rows(fn, "y", y, n_out)
+    i32 = _torch.int32
     E = offsets.shape[0] - 1
-    _packed(fn, "offsets", offsets, (E + 1,), torch.int32)
-    M = y.shape[0]
+    _packed(fn, "offsets", offsets, (E + 1,), i32)
+    rows = M = y.shape[0]
     if perm is not None:
         M = perm.shape[0]
-        _packed(fn, "perm", perm, (M,), torch.int32)
+        _packed(fn, "perm", perm, (M,), i32)
     if entry_of is not None:
-        _packed(fn, "entry_of", entry_of, (E,), torch.int32)
+        _packed(fn, "entry_of", entry_of, (E,), i32)
     if gate is not None:
-        _packed(fn, "gate", gate, gate.shape, torch.float32)
+        _packed(fn, "gate", gate, gate.shape, _torch.float32)
     if x_perm is None:
         x_perm = perm is not None
     d = _device(fn, x, w, offsets, y, x_scale, w_scale, y_scale, perm, gate, entry_of)
-    g = Grouped(xf, wf, yf, int(bool(swiglu)), E, M, w.shape[1], K, x.shape[0], x_div, y.shape[0], int(bool(x_perm)),
-                int(bool(y_perm)), 0 if gate is None else gate.numel(), ldx, ldy, w.shape[0], _ptr(x), _ptr(x_scale), _ptr(w), _ptr(w_scale), _ptr(y),
-                _ptr(y_scale), _ptr(offsets), _ptr(perm), _ptr(entry_of), _ptr(gate))
-    st, ctx = _on(d, stream)
-    with ctx:
-        _check("mc_grouped_matmul", lib().mc_grouped_matmul(C.byref(g), st))
+    g = Grouped(xf, wf, yf, 1 if swiglu else 0, E, M, N, K, x.shape[0], x_div, rows, 1 if x_perm else 0,
+                1 if y_perm else 0, 0 if gate is None else gate.numel(), ldx, ldy, n, x.data_ptr(), _ptr(x_scale),
+                w.data_ptr(), _ptr(w_scale), y.data_ptr(), _ptr(y_scale), offsets.data_ptr(), _ptr(perm),
+                _ptr(entry_of), _ptr(gate))
+    _call("mc_grouped_matmul", d, stream, lib().mc_grouped_matmul, C.byref(g))
 
 
 def prefill_act_ws_bytes(T: int, k: int, E: int, H: int, I: int, act: str) -> int:
@@ -558,27 +569,27 @@ def moe_experts_prefill_act(x, ids, w, n_tok, E: int, layer_buf: Banks, act: str
                             nxt: Optional[Prefetch] = None, stream=None) -> None:
     """Prefill layer on bf16 or MXFP4 activations (act = "bf16" or "mxfp4"): x and y bf16 (values or
     bits) [T][H], ids int32 and w fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes."""
-    import torch
     fn = "moe_experts_prefill_act"
     if act not in FMT:
         raise ValueError("%s: act must be bf16 or mxfp4, not %r" % (fn, act))
     if ids.dim() != 2:
         raise ValueError("%s: ids has shape %s" % (fn, tuple(ids.shape)))
     T, k = ids.shape
-    _packed(fn, "ids", ids, (T, k), torch.int32)
-    _packed(fn, "w", w, (T, k), torch.float32)
+    if _torch is None:
+        _load_torch()
+    _packed(fn, "ids", ids, (T, k), _torch.int32)
+    _packed(fn, "w", w, (T, k), _torch.float32)
     for what, t in (("x", x), ("y", y)):
         if _etype(t) != MC_BF16:
             raise ValueError("%s: %s must be bf16, not %s" % (fn, what, t.dtype))
         _packed(fn, what, t, (T, layer_buf.H), t.dtype)
     if n_tok is not None:
-        _packed(fn, "n_tok", n_tok, (1,), torch.int32)
+        _packed(fn, "n_tok", n_tok, (1,), _torch.int32)
     d = _device(fn, x, ids, w, n_tok, ws, y)
-    st, ctx = _on(d, stream)
-    with ctx:
-        _check(fn, lib().moe_experts_prefill_act(
-            _ptr(x), _ptr(ids), _ptr(w), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], _ptr(ws),
-            ws.numel() * ws.element_size(), _ptr(y), st, C.byref(nxt) if nxt is not None else None))
+    f = lib().moe_experts_prefill_act
+    _call(fn, d, stream, lambda st: f(
+        _ptr(x), _ptr(ids), _ptr(w), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], _ptr(ws),
+        ws.numel() * ws.element_size(), _ptr(y), st, C.byref(nxt) if nxt is not None else None))
 
 
 class HostPool:

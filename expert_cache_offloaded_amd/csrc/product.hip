@@ -188,6 +188,12 @@ __device__ __forceinline__ void store_pair(const ProductArgs& a, const RowOut& o
   }
 }
 
+// One 16-column fragment (bf16 or fp32 y).
+__device__ __forceinline__ void store_one(const ProductArgs& a, const RowOut& o, int col0, int n_out, f32x4_t v) {
+  const int col = col0 + 4 * ((threadIdx.x & 63) >> 4);
+  if (o.y >= 0 && col < n_out) store4(a, o.y, col, n_out, a.gate ? o.gate * v : v);
+}
+
 __device__ __forceinline__ f32x4_t swiglu4(const f32x4_t& g, const f32x4_t& u) {
   f32x4_t h;
 #pragma unroll
@@ -209,85 +215,123 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t w, uint32_t sw, u32x4_t x, u
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, c, 4, 4, 0, (int)sw, 0, (int)sx);
 }
 
-// ---------------------------------------------------------------- the kernel
+// ---------------------------------------------------------------- few rows
 //
-// 64 rows x 64 weight rows (SwiGLU: 32 gate and the matching 32 up rows) per workgroup of 4
-// waves; a wave multiplies 16 rows with all 64 weight rows, operands straight from memory.
+// Tiles of 16 MF rows x 16 NT weight rows (SwiGLU: NT / 2 fragments of gate rows and the matching
+// up rows), NT x KW waves: a wave multiplies one 16-row weight fragment over every KW-th
+// step of K (64 bytes of each weight row per step), operands straight from memory, and the KW
+// partial sums meet in LDS in a fixed order.  With few rows the weights are read once and bound
+// the product; what counts is that all of a wave's loads are on their way at once (kFewSteps steps
+// per round) and that even a small matrix fills the chip, hence the split of K over waves
+// and the narrow tiles.
 
-constexpr int kBM = 64, kBN = 64;
+constexpr int kFewSteps = 4;
 
-template <int XF, int WF>
-__global__ void __launch_bounds__(256)
-product_kernel(ProductArgs a, int n_nb) {
+template <int XF, int WF, int MF, int NT, int KW>
+__global__ void __launch_bounds__(64 * NT * KW)
+product_few_kernel(ProductArgs a, int n_nb) {
+  __shared__ f32x4_t part[KW][NT][MF][64];
   Tile t;
-  if (!find_tile<kBM, false>(a, blockIdx.x, n_nb, &t)) return;
+  if (!find_tile<16 * MF, false>(a, blockIdx.x, n_nb, &t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
-  if (wave * 16 >= t.nrows) return;
+  const int f = wave % NT, kw = wave / NT;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
-  const int cols = a.swiglu ? kBN / 2 : kBN;        // output columns of a tile
-  const int c0 = t.nb * cols;
+  const int c0 = t.nb * (a.swiglu ? 8 * NT : 16 * NT);
   const int64_t K = a.K;
   const int64_t wrow_b = WF == MC_BF16 ? 2 * K : K / 2, xrow_b = XF == MC_BF16 ? 2 * a.ldx : K / 2;
-  const uint8_t* wp[4];
-  const uint8_t* wsp[4];
+  const int nblk = a.K / 32;
+  const int steps = WF == MC_BF16 ? nblk : (nblk + 3) / 4;
+  const int wrow = a.swiglu ? min(c0 + (f % (NT / 2)) * 16 + l16, n_out - 1) + (f >= NT / 2 ? n_out : 0)
+                            : min(c0 + f * 16 + l16, n_out - 1);
+  const uint8_t* wp = a.w + ((int64_t)t.entry * a.N + wrow) * wrow_b;
+  const uint8_t* wsp = a.ws + ((int64_t)t.entry * a.N + wrow) * (K / 32);
+  const uint8_t* xp[MF];
+  const uint8_t* xsp[MF];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) {
-    int row = a.swiglu ? c0 + (f & 1) * 16 + l16 : c0 + f * 16 + l16;
-    row = min(row, n_out - 1) + (a.swiglu && f >= 2 ? n_out : 0);
-    const int64_t wr = (int64_t)t.entry * a.N + row;
-    wp[f] = a.w + wr * wrow_b;
-    wsp[f] = a.ws + wr * (K / 32);
+  for (int m = 0; m < MF; ++m) {
+    const int i = t.row0 + min(16 * m + l16, t.nrows - 1);
+    const int64_t xr = max(x_row(a, i, a.perm ? a.perm[i] : i), 0);
+    xp[m] = a.x + xr * xrow_b;
+    xsp[m] = a.xs + xr * (K / 32);
   }
-  const int m = wave * 16 + l16;
-  const int i_row = t.row0 + min(m, t.nrows - 1);
-  const int64_t xr = max(x_row(a, i_row, a.perm ? a.perm[i_row] : i_row), 0);
-  const uint8_t* xp = a.x + xr * xrow_b;
-  const uint8_t* xsp = a.xs + xr * (K / 32);
 
-  f32x4_t acc[4];
+  f32x4_t acc[MF];
 #pragma unroll
-  for (int f = 0; f < 4; ++f) acc[f] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  if (WF == MC_BF16) {
-    for (int64_t k = 0; k < 2 * K; k += 64) {
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp + k + 16 * g);
+  for (int m = 0; m < MF; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = kw; s0 < steps; s0 += KW * kFewSteps) {
+    u32x4_t w[kFewSteps];
+    uint32_t sw[kFewSteps];
+    // steps and blocks past the end re-read the last ones and count as zeros
 #pragma unroll
-      for (int f = 0; f < 4; ++f) acc[f] = mfma_bf16(*reinterpret_cast<const u32x4_t*>(wp[f] + k + 16 * g), x, acc[f]);
-    }
-  } else {
-    const int nblk = a.K / 32;
-    for (int b0 = 0; b0 < nblk; b0 += 4) {
-      const int b = b0 + g;
-      const bool in = b < nblk;                     // blocks past K count as zeros
-      u32x4_t w[4];
-      uint32_t sw[4];
-#pragma unroll
-      for (int f = 0; f < 4; ++f) {
-        w[f] = in ? *reinterpret_cast<const u32x4_t*>(wp[f] + (int64_t)b * 16) : u32x4_t{0, 0, 0, 0};
-        sw[f] = in ? wsp[f][b] : 127u;
-      }
-      if (XF == MC_MXFP4) {
-        const u32x4_t x = in ? *reinterpret_cast<const u32x4_t*>(xp + (int64_t)b * 16) : u32x4_t{0, 0, 0, 0};
-        const uint32_t sx = in ? xsp[b] : 127u;
-#pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f] = mfma_fp4(w[f], sw[f], x, sx, acc[f]);
+    for (int u = 0; u < kFewSteps; ++u) {
+      const int s = min(s0 + u * KW, steps - 1);
+      if (WF == MC_BF16) {
+        w[u] = *reinterpret_cast<const u32x4_t*>(wp + (int64_t)s * 64 + 16 * g);
       } else {
-        // the K order of the four products is permuted: lane group g holds block b0 + g
+        const int b = min(4 * s + g, nblk - 1);
+        w[u] = *reinterpret_cast<const u32x4_t*>(wp + (int64_t)b * 16);
+        sw[u] = wsp[b];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kFewSteps; ++u) {
+      const int s = min(s0 + u * KW, steps - 1);
+      const bool in = s0 + u * KW < steps && (WF == MC_BF16 || 4 * s + g < nblk);
+      const int b = WF == MC_BF16 ? s : min(4 * s + g, nblk - 1);
+      if (!in) w[u] = u32x4_t{0, 0, 0, 0};
+      if (WF == MC_BF16) {
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+          u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 64 + 16 * g);
+          if (!in) x = u32x4_t{0, 0, 0, 0};       // a zero times an infinity is no zero
+          acc[m] = mfma_bf16(w[u], x, acc[m]);
+        }
+      } else if (XF == MC_MXFP4) {
+        if (!in) sw[u] = 127u;
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 16);
+          const uint32_t sx = in ? xsp[m][b] : 127u;
+          acc[m] = mfma_fp4(w[u], sw[u], x, sx, acc[m]);
+        }
+      } else {
+        // the K order of the four products is permuted: lane group g holds block b of its row
+        const float s32 = in ? e8m0_or_nan(sw[u]) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const u32x4_t x = in ? *reinterpret_cast<const u32x4_t*>(xp + (int64_t)b * 64 + 16 * j) : u32x4_t{0, 0, 0, 0};
+          const u32x4_t wj = __builtin_bit_cast(u32x4_t, fp4x8_bf16(w[u][j], s32));
 #pragma unroll
-          for (int f = 0; f < 4; ++f)
-            acc[f] = mfma_bf16(__builtin_bit_cast(u32x4_t, fp4x8_bf16(w[f][j], e8m0_or_nan(sw[f]))), x, acc[f]);
+          for (int m = 0; m < MF; ++m) {
+            u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 64 + 16 * j);
+            if (!in) x = u32x4_t{0, 0, 0, 0};
+            acc[m] = mfma_bf16(wj, x, acc[m]);
+          }
         }
       }
     }
   }
-  const RowOut o = row_out(a, i_row, m < t.nrows);
-  if (a.swiglu) {
-    store_pair(a, o, c0, n_out, swiglu4(acc[0], acc[2]), swiglu4(acc[1], acc[3]));
-  } else {
-    store_pair(a, o, c0, n_out, acc[0], acc[1]);
-    store_pair(a, o, c0 + 32, n_out, acc[2], acc[3]);
+#pragma unroll
+  for (int m = 0; m < MF; ++m) part[kw][f][m][lane] = acc[m];
+  __syncthreads();
+  // the partial sums of a row fragment: wave m < MF takes row fragment m (and all columns)
+  for (int m = wave; m < MF; m += NT * KW) {
+    const int r = 16 * m + l16;
+    if (16 * m >= t.nrows) break;
+    f32x4_t v[NT];
+#pragma unroll
+    for (int q = 0; q < NT; ++q) {
+      v[q] = part[0][q][m][lane];
+#pragma unroll
+      for (int k = 1; k < KW; ++k) v[q] += part[k][q][m][lane];
+    }
+    const RowOut o = row_out(a, t.row0 + min(r, t.nrows - 1), r < t.nrows);
+    if (a.swiglu) {
+      if (NT == 4) store_pair(a, o, c0, n_out, swiglu4(v[0], v[2]), swiglu4(v[1], v[3]));
+      else store_one(a, o, c0, n_out, swiglu4(v[0], v[1]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < NT; q += 2) store_pair(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
+    }
   }
 }
 
@@ -599,32 +643,66 @@ int check_product(const char* fn, const ProductArgs& a) {
   return MC_OK;
 }
 
-int launch_product(const ProductArgs& a, hipStream_t s) {
-  if (a.M == 0 || a.N == 0 || a.x_rows == 0 || a.y_rows == 0 || a.n == 0) return MC_OK;
-  const bool wide = a.M > 32;
-  const int64_t bm = wide ? kWideBM : kBM, bn = wide ? kWideBN : kBN;
-  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? bn / 2 : bn;
+// Row tiles of all groups together, at most: sum over groups of ceil(rows / bm).
+static int64_t most_row_tiles(const ProductArgs& a, int64_t bm) {
+  return a.offsets ? a.M / bm + (a.E < a.M ? a.E : a.M) : (a.M + bm - 1) / bm;
+}
+
+template <int XF, int WF, int MF, int NT>
+static void launch_few_k(const ProductArgs& a, unsigned grid, int n_nb, int steps, hipStream_t s) {
+  // enough waves along K that a wave has at most 4 steps, up to 16 waves per workgroup
+  if (steps <= 16 || NT == 4)
+    hipLaunchKernelGGL((product_few_kernel<XF, WF, MF, NT, 4>), dim3(grid), dim3(64 * NT * 4), 0, s, a, n_nb);
+  else if constexpr (NT == 2)
+    hipLaunchKernelGGL((product_few_kernel<XF, WF, MF, NT, 8>), dim3(grid), dim3(64 * NT * 8), 0, s, a, n_nb);
+}
+
+template <int XF, int WF>
+static int launch_few(const ProductArgs& a, hipStream_t s) {
+  const int nt = a.swiglu && a.y_fmt == MC_MXFP4 ? 4 : 2;
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? 8 * nt : 16 * nt;
   const int64_t n_nb = (n_out + cols - 1) / cols;
-  // sum over groups of ceil(rows / bm)
-  const int64_t mt = a.offsets ? a.M / bm + (a.E < a.M ? a.E : a.M) : (a.M + bm - 1) / bm;
-  MC_REQUIRE(mt * n_nb <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
-  const dim3 grid((unsigned)(mt * n_nb)), block(wide ? kWideThreads : 256);
-  const int nb = (int)n_nb;
-  if (wide) {
-    const bool sdma = a.K % 128 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 4 == 0;
-    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, block, 0, s, a, nb); };
-    if (a.w_fmt == MC_BF16) run(product_wide_kernel<kBf16, true>);
-    else if (a.x_fmt == MC_BF16 && sdma) run(product_wide_kernel<kA16W4, true>);
-    else if (a.x_fmt == MC_BF16) run(product_wide_kernel<kA16W4, false>);
-    else if (sdma) run(product_wide_kernel<kFp4, true>);
-    else run(product_wide_kernel<kFp4, false>);
+  const int mf = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
+  const int64_t tiles = most_row_tiles(a, 16 * mf) * n_nb;
+  MC_REQUIRE(tiles <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
+  const int steps = WF == MC_BF16 ? a.K / 32 : (a.K + 127) / 128;
+  const unsigned grid = (unsigned)tiles;
+  if (nt == 4) {
+    if (mf == 1) launch_few_k<XF, WF, 1, 4>(a, grid, (int)n_nb, steps, s);
+    else if (mf == 2) launch_few_k<XF, WF, 2, 4>(a, grid, (int)n_nb, steps, s);
+    else launch_few_k<XF, WF, 4, 4>(a, grid, (int)n_nb, steps, s);
   } else {
-    if (a.x_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_MXFP4, MC_MXFP4>), grid, block, 0, s, a, nb);
-    else if (a.w_fmt == MC_MXFP4) hipLaunchKernelGGL((product_kernel<MC_BF16, MC_MXFP4>), grid, block, 0, s, a, nb);
-    else hipLaunchKernelGGL((product_kernel<MC_BF16, MC_BF16>), grid, block, 0, s, a, nb);
+    if (mf == 1) launch_few_k<XF, WF, 1, 2>(a, grid, (int)n_nb, steps, s);
+    else if (mf == 2) launch_few_k<XF, WF, 2, 2>(a, grid, (int)n_nb, steps, s);
+    else launch_few_k<XF, WF, 4, 2>(a, grid, (int)n_nb, steps, s);
   }
   MC_LAUNCH_CHECK();
   return MC_OK;
+}
+
+static int launch_wide(const ProductArgs& a, hipStream_t s) {
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? kWideBN / 2 : kWideBN;
+  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, kWideBM) * n_nb;
+  MC_REQUIRE(tiles <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
+  const bool sdma = a.K % 128 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 4 == 0;
+  auto run = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kWideThreads), 0, s, a, (int)n_nb);
+  };
+  if (a.w_fmt == MC_BF16) run(product_wide_kernel<kBf16, true>);
+  else if (a.x_fmt == MC_BF16 && sdma) run(product_wide_kernel<kA16W4, true>);
+  else if (a.x_fmt == MC_BF16) run(product_wide_kernel<kA16W4, false>);
+  else if (sdma) run(product_wide_kernel<kFp4, true>);
+  else run(product_wide_kernel<kFp4, false>);
+  MC_LAUNCH_CHECK();
+  return MC_OK;
+}
+
+int launch_product(const ProductArgs& a, hipStream_t s) {
+  if (a.M == 0 || a.N == 0 || a.x_rows == 0 || a.y_rows == 0 || a.n == 0) return MC_OK;
+  if (a.M > 64) return launch_wide(a, s);
+  if (a.x_fmt == MC_MXFP4) return launch_few<MC_MXFP4, MC_MXFP4>(a, s);
+  if (a.w_fmt == MC_MXFP4) return launch_few<MC_BF16, MC_MXFP4>(a, s);
+  return launch_few<MC_BF16, MC_BF16>(a, s);
 }
 
 }  // namespace mc
