@@ -22,9 +22,10 @@ struct Tile {
 
 // Group e's first row and row count (offsets clamped into [0, M], 0 rows if its entry is
 // outside the matrices).
-__device__ __forceinline__ int group_rows(const ProductArgs& a, int e, int* lo) {
-  const int b = min(max(a.offsets[e], 0), a.M), t = min(max(a.offsets[e + 1], 0), a.M);
-  const int en = a.entry_of ? a.entry_of[e] : e;
+template <class P>
+__device__ __forceinline__ int group_rows(const ProductArgs& a, P offsets, P entry_of, int e, int* lo) {
+  const int b = min(max(offsets[e], 0), a.M), t = min(max(offsets[e + 1], 0), a.M);
+  const int en = entry_of ? entry_of[e] : e;
   *lo = b;
   return en >= 0 && en < a.n ? max(t - b, 0) : 0;
 }
@@ -46,64 +47,106 @@ __device__ __forceinline__ void tile_place(int p, int m, int n_nb, int* mt, int*
   *mt = band * 8 + in - *nb * h;
 }
 
-// Tile of workgroup `b` (XCD: dealt out by xcd_order): row tiles of BM rows, group by group.
-// Every wave runs the search by itself: lane l looks at group 64 c + l, a prefix sum over the
-// lanes gives each group's first tile.
-template <int BM, bool XCD>
+__device__ __forceinline__ constexpr int div_up(int a, int b) { return (a + b - 1) / b; }
+
+// Sum over the lanes up to and including this one.
+__device__ __forceinline__ int lane_prefix(int v) {
+  // row_shr 1, 2, 4, 8, then the rows' totals to the rows behind them
+#define MC_STEP(CTRL, ROWS) v += __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false)
+  MC_STEP(0x111, 0xF);
+  MC_STEP(0x112, 0xF);
+  MC_STEP(0x114, 0xF);
+  MC_STEP(0x118, 0xF);
+  MC_STEP(0x142, 0xA);
+  MC_STEP(0x143, 0xC);
+#undef MC_STEP
+  return v;
+}
+
+// The row tile j (BM rows) of all groups: its group's tiles begin at `first`.
+__device__ __forceinline__ void place_in_group(const ProductArgs& a, int e, int p, int bm, int n_nb, Tile* t) {
+  // e is the same for the wave: scalar loads, which no vector load's wait holds up (the tables are
+  // not written while the kernel runs)
+  typedef const __attribute__((address_space(4))) int32_t* scalar_ptr;
+  const scalar_ptr offsets = (scalar_ptr)a.offsets, entry_of = (scalar_ptr)a.entry_of;
+  int lo;
+  const int rows = group_rows(a, offsets, entry_of, e, &lo);
+  int mt;
+  tile_place(p, div_up(rows, bm), n_nb, &mt, &t->nb);
+  t->row0 = lo + mt * bm;
+  t->nrows = min(bm, rows - mt * bm);
+  t->entry = a.entry_of ? entry_of[e] : e;
+}
+
+__device__ __forceinline__ void place_ungrouped(const ProductArgs& a, int p, int bm, int n_nb, Tile* t) {
+  int mt;
+  tile_place(p, div_up(a.M, bm), n_nb, &mt, &t->nb);
+  t->entry = 0;
+  t->row0 = mt * bm;
+  t->nrows = min(bm, a.M - t->row0);
+}
+
+// Tile b of the call, group by group.  Every wave runs the search by itself: lane l looks at group
+// 64 c + l, a prefix sum over the lanes gives each group's first tile.
+template <int BM>
 __device__ __forceinline__ bool find_tile(const ProductArgs& a, int b, int n_nb, Tile* t) {
   if (!a.offsets) {
-    const int m = (a.M + BM - 1) / BM;
-    if (b >= m * n_nb) return false;
-    int mt;
-    tile_place(XCD ? xcd_order(b, m * n_nb) : b, m, n_nb, &mt, &t->nb);
-    t->entry = 0;
-    t->row0 = mt * BM;
-    t->nrows = min(BM, a.M - t->row0);
+    if (b >= div_up(a.M, BM) * n_nb) return false;
+    place_ungrouped(a, b, BM, n_nb, t);
     return true;
   }
   const int lane = threadIdx.x & 63;
-  int L = b;
-  if (XCD) {
-    int m = 0;
-    for (int e = lane; e < a.E; e += 64) {
-      int lo;
-      m += (group_rows(a, e, &lo) + BM - 1) / BM;
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m += __shfl_xor(m, o, 64);
-    const int total = __builtin_amdgcn_readfirstlane(m) * n_nb;
-    if (b >= total) return false;
-    L = xcd_order(b, total);
-  }
-  const int j = L / n_nb;
+  const int j = b / n_nb;
   int before = 0;
   for (int base = 0; base < a.E; base += 64) {
     const int e = base + lane;
-    int lo = 0;
-    const int rows = e < a.E ? group_rows(a, e, &lo) : 0;
-    const int m = (rows + BM - 1) / BM;
-    int incl = m;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, 64);
-      if (lane >= o) incl += v;
-    }
+    int lo;
+    const int m = e < a.E ? div_up(group_rows(a, a.offsets, a.entry_of, e, &lo), BM) : 0;
+    const int incl = lane_prefix(m);
     const uint64_t past = __ballot(before + incl > j);
     if (past) {
       const int src = __ffsll((unsigned long long)past) - 1;
       const int first = before + __builtin_amdgcn_readlane(incl - m, src);
-      const int me = __builtin_amdgcn_readlane(m, src), lo_e = __builtin_amdgcn_readlane(lo, src);
-      const int rows_e = __builtin_amdgcn_readlane(rows, src);
-      int mt;
-      tile_place(L - first * n_nb, me, n_nb, &mt, &t->nb);
-      t->row0 = lo_e + mt * BM;
-      t->nrows = min(BM, rows_e - mt * BM);
-      t->entry = a.entry_of ? a.entry_of[base + src] : base + src;
+      place_in_group(a, base + src, b - first * n_nb, BM, n_nb, t);
       return true;
     }
     before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
+}
+
+// The same with the groups' first tiles in LDS, for workgroups that take several tiles: after
+// first_tiles (one wave) and a barrier, first[e] is group e's first row tile, first[E] their number.
+template <int BM>
+__device__ __forceinline__ void first_tiles(const ProductArgs& a, int* first) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int base = 0; base < a.E; base += 64) {
+    const int e = base + lane;
+    int lo;
+    const int m = e < a.E ? div_up(group_rows(a, a.offsets, a.entry_of, e, &lo), BM) : 0;
+    const int incl = lane_prefix(m);
+    if (e < a.E) first[e] = before + incl - m;
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  if (lane == 0) first[a.E] = before;
+}
+
+// Tile b in the order of the XCDs (total: tiles of the call).
+template <int BM>
+__device__ __forceinline__ void next_tile(const ProductArgs& a, int b, int total, int n_nb, const int* first, Tile* t) {
+  const int L = xcd_order(b, total);
+  if (!a.offsets) return place_ungrouped(a, L, BM, n_nb, t);
+  const int lane = threadIdx.x & 63;
+  const int j = L / n_nb;
+  for (int base = 0;; base += 64) {                // first[E] > j, so a group is found
+    const uint64_t past = __ballot(first[min(base + lane, a.E - 1) + 1] > j);
+    if (past) {
+      const int e = base + __ffsll((unsigned long long)past) - 1;
+      place_in_group(a, e, L - __builtin_amdgcn_readfirstlane(first[e]) * n_nb, BM, n_nb, t);
+      return;
+    }
+  }
 }
 
 // Row of x of sorted row i whose route is r; -1 if it is outside x.
@@ -113,85 +156,132 @@ __device__ __forceinline__ int x_row(const ProductArgs& a, int i, int r) {
   return r >= 0 && xr < a.x_rows ? xr : -1;
 }
 
-// Four results v of columns col .. col + 3 of row y_row of y.
-__device__ __forceinline__ void store4(const ProductArgs& a, int64_t row, int col, int n_out, const f32x4_t& v) {
-  if (a.y_fmt == MC_F32) {
-    float* p = reinterpret_cast<float*>(a.y) + row * a.ldy + col;
-    if (col + 4 <= n_out && (a.ldy & 3) == 0) {
-      *reinterpret_cast<f32x4_t*>(p) = v;
+// fp32 -> bf16 pairs, round to nearest even (one instruction per pair).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const bf16x2_t r = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, r);
+}
+
+// N (4 or 8) results of columns col .. col + N - 1 of a row of y that starts at p.  YF: y's type; VEC:
+// rows and columns allow vector stores.
+template <int YF, bool VEC, int N>
+__device__ __forceinline__ void store_cols(uint8_t* p, int col, int n_out, const float* v) {
+  if (YF == MC_F32) {
+    float* q = reinterpret_cast<float*>(p) + col;
+    if (VEC && col + N <= n_out) {
+#pragma unroll
+      for (int i = 0; i < N; i += 4) *reinterpret_cast<f32x4_t*>(q + i) = f32x4_t{v[i], v[i + 1], v[i + 2], v[i + 3]};
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + i < n_out) p[i] = v[i];
+      for (int i = 0; i < N; ++i)
+        if (col + i < n_out) q[i] = v[i];
     }
   } else {
-    uint16_t* p = reinterpret_cast<uint16_t*>(a.y) + row * a.ldy + col;
-    uint16_t o[4];
+    uint16_t* q = reinterpret_cast<uint16_t*>(p) + col;
+    uint32_t c[N / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = f32_to_bf16_rne(v[i]);
-    if (col + 4 <= n_out && (a.ldy & 3) == 0) {
-      *reinterpret_cast<uint2*>(p) = make_uint2(o[0] | ((uint32_t)o[1] << 16), o[2] | ((uint32_t)o[3] << 16));
+    for (int i = 0; i < N / 2; ++i) c[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+    if (VEC && col + N <= n_out) {
+      __builtin_memcpy(__builtin_assume_aligned(q, 2 * N), c, 2 * N);
     } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (col + i < n_out) p[i] = o[i];
+      for (int i = 0; i < N; ++i)
+        if (col + i < n_out) q[i] = (uint16_t)(c[i / 2] >> (16 * (i & 1)));
     }
   }
 }
 
-// Where sorted row i goes: its row of y (-1: nowhere) and its gate.
+// Where a sorted row goes: its row of y (-1: nowhere) and its gate.
 struct RowOut {
   int64_t y;
   float gate;
 };
 
-__device__ __forceinline__ RowOut row_out(const ProductArgs& a, int i, bool on) {
-  const int r = a.perm ? a.perm[i] : i;
-  const int yr = a.y_perm ? r : i;
-  on = on && r >= 0 && x_row(a, i, r) >= 0 && yr < a.y_rows && (!a.gate || r < a.n_gate);
-  return RowOut{on ? yr : -1, a.gate && on ? a.gate[r] : 1.0f};
+// The rows i[m] (those with !on[m] go nowhere).  Every route is read before the first gate, and every
+// gate before the first result is stored: no chain of round trips row by row.
+template <int N>
+__device__ __forceinline__ void rows_out(const ProductArgs& a, const int* i, const bool* on, RowOut* o) {
+  int r[N];
+  if (a.perm) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) r[m] = a.perm[i[m]];
+  } else {
+#pragma unroll
+    for (int m = 0; m < N; ++m) r[m] = i[m];
+  }
+  // r / x_div < x_rows without the division
+  const int64_t most = a.x_perm ? (int64_t)a.x_rows * a.x_div : INT64_MAX;
+#pragma unroll
+  for (int m = 0; m < N; ++m) {
+    const int yr = a.y_perm ? r[m] : i[m];
+    const bool to = on[m] && r[m] >= 0 && r[m] < most && (a.x_perm || i[m] < a.x_rows) && yr < a.y_rows &&
+                    (!a.gate || r[m] < a.n_gate);
+    o[m] = RowOut{to ? yr : -1, 1.0f};
+    if (!to) r[m] = 0;
+  }
+  if (a.gate && a.n_gate > 0) {
+#pragma unroll
+    for (int m = 0; m < N; ++m) o[m].gate = a.gate[r[m]];
+  }
 }
 
-// Two 16-column fragments v (32 neighbouring columns from col0) of one 16-row fragment: v[f][i] is
-// column col0 + 16 f + 4 (lane / 16) + i of the lane's row (lane % 16 of the fragment).
-__device__ __forceinline__ void store_pair(const ProductArgs& a, const RowOut& o, int col0, int n_out, f32x4_t v0,
-                                           f32x4_t v1) {
+// Two 16-column fragments (32 neighbouring columns from col0) of one 16-row fragment: vf[i] is column
+// col0 + 16 f + 4 (lane / 16) + i of the lane's row (lane % 16 of the fragment).
+template <int YF, bool VEC>
+__device__ __forceinline__ void store_pair(const ProductArgs& a, const RowOut& o, int col0, int n_out,
+                                           const f32x4_t& v0, const f32x4_t& v1) {
   const int g = (threadIdx.x & 63) >> 4;
-  if (a.gate) {
-    v0 *= o.gate;
-    v1 *= o.gate;
+  // lane quarters 1 and 3 of the first fragment change places with 0 and 2 of the second: a lane
+  // then holds eight neighbouring columns, 8 (g / 2) of fragment g % 2
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v0[i]), __float_as_uint(v1[i]), false, false);
+    v[i] = o.gate * __uint_as_float(s[0]);        // 1 without gates
+    v[4 + i] = o.gate * __uint_as_float(s[1]);
   }
-  if (a.y_fmt == MC_MXFP4) {
-    // the block's 8 quarters of four columns meet by lane exchanges over lane bits 4 and 5
-    float e[8];
+  const int col = col0 + 16 * (g & 1) + 8 * (g >> 1);
+  if (YF == MC_MXFP4) {
+    // the block's four lanes meet by lane exchanges over lane bits 4 and 5
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      e[i] = v0[i];
-      e[4 + i] = v1[i];
-      m = max(m, max(abs_bits(v0[i]), abs_bits(v1[i])));
-    }
+    for (int i = 0; i < 8; ++i) m = max(m, abs_bits(v[i]));
     m = max(m, (uint32_t)__shfl_xor((int)m, 16, 64));
     m = max(m, (uint32_t)__shfl_xor((int)m, 32, 64));
     const uint32_t X = block_exponent(m);
-    const uint32_t c = fp4x8_codes(e, X);
+    const uint32_t c = fp4x8_codes(v, X);
     if (o.y >= 0 && col0 < n_out) {
-      uint8_t* p = a.y + o.y * (int64_t)(n_out / 2) + (col0 >> 1) + 2 * g;
-      *reinterpret_cast<uint16_t*>(p) = (uint16_t)c;
-      *reinterpret_cast<uint16_t*>(p + 8) = (uint16_t)(c >> 16);
+      *reinterpret_cast<uint32_t*>(a.y + o.y * (int64_t)(n_out / 2) + (col >> 1)) = c;
       if (g == 0) a.ys[o.y * (int64_t)(n_out / 32) + (col0 >> 5)] = (uint8_t)X;
     }
-  } else if (o.y >= 0) {
-    const int col = col0 + 4 * g;
-    if (col < n_out) store4(a, o.y, col, n_out, v0);
-    if (col + 16 < n_out) store4(a, o.y, col + 16, n_out, v1);
+  } else if (o.y >= 0 && col < n_out) {
+    store_cols<YF, VEC, 8>(a.y + o.y * a.ldy * (YF == MC_F32 ? 4 : 2), col, n_out, v);
   }
 }
 
 // One 16-column fragment (bf16 or fp32 y).
-__device__ __forceinline__ void store_one(const ProductArgs& a, const RowOut& o, int col0, int n_out, f32x4_t v) {
+template <int YF, bool VEC>
+__device__ __forceinline__ void store_one(const ProductArgs& a, const RowOut& o, int col0, int n_out,
+                                          const f32x4_t& f) {
   const int col = col0 + 4 * ((threadIdx.x & 63) >> 4);
-  if (o.y >= 0 && col < n_out) store4(a, o.y, col, n_out, a.gate ? o.gate * v : v);
+  const float v[4] = {o.gate * f[0], o.gate * f[1], o.gate * f[2], o.gate * f[3]};
+  if (YF != MC_MXFP4 && o.y >= 0 && col < n_out)
+    store_cols<YF, VEC, 4>(a.y + o.y * a.ldy * (YF == MC_F32 ? 4 : 2), col, n_out, v);
+}
+
+// f(type of y, rows aligned for vector stores) with both as constants: the branches are taken once.
+template <int V>
+struct Const {
+  static constexpr int value = V;
+};
+template <class F>
+__device__ __forceinline__ void with_format(const ProductArgs& a, F f) {
+  const bool vec = (a.ldy & 7) == 0;
+  if (a.y_fmt == MC_MXFP4) f(Const<MC_MXFP4>(), Const<1>());
+  else if (a.y_fmt == MC_F32 && vec) f(Const<MC_F32>(), Const<1>());
+  else if (a.y_fmt == MC_F32) f(Const<MC_F32>(), Const<0>());
+  else if (vec) f(Const<MC_BF16>(), Const<1>());
+  else f(Const<MC_BF16>(), Const<0>());
 }
 
 __device__ __forceinline__ f32x4_t swiglu4(const f32x4_t& g, const f32x4_t& u) {
@@ -232,7 +322,7 @@ __global__ void __launch_bounds__(64 * NT * KW)
 product_few_kernel(ProductArgs a, int n_nb) {
   __shared__ f32x4_t part[KW][NT][MF][64];
   Tile t;
-  if (!find_tile<16 * MF, false>(a, blockIdx.x, n_nb, &t)) return;
+  if (!find_tile<16 * MF>(a, blockIdx.x, n_nb, &t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int f = wave % NT, kw = wave / NT;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
@@ -324,43 +414,55 @@ product_few_kernel(ProductArgs a, int n_nb) {
 #pragma unroll
       for (int k = 1; k < KW; ++k) v[q] += part[k][q][m][lane];
     }
-    const RowOut o = row_out(a, t.row0 + min(r, t.nrows - 1), r < t.nrows);
-    if (a.swiglu) {
-      if (NT == 4) store_pair(a, o, c0, n_out, swiglu4(v[0], v[2]), swiglu4(v[1], v[3]));
-      else store_one(a, o, c0, n_out, swiglu4(v[0], v[1]));
-    } else {
+    const int i = t.row0 + min(r, t.nrows - 1);
+    const bool on = r < t.nrows;
+    RowOut o;
+    rows_out<1>(a, &i, &on, &o);
+    with_format(a, [&](auto yf, auto vec) {
+      constexpr int YF = decltype(yf)::value;
+      constexpr bool VEC = decltype(vec)::value;
+      if (a.swiglu) {
+        if (NT == 4) store_pair<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[NT / 2]), swiglu4(v[1], v[NT / 2 + 1 < NT ? NT / 2 + 1 : 0]));
+        else store_one<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[1]));
+      } else {
 #pragma unroll
-      for (int q = 0; q < NT; q += 2) store_pair(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
-    }
+        for (int q = 0; q < NT; q += 2) store_pair<YF, VEC>(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
+      }
+    });
   }
 }
 
 // ---------------------------------------------------------------- many rows
 //
-// 256 rows x 256 weight rows (SwiGLU: 128 gate and the matching 128 up rows) per workgroup of 8
-// waves, 2 along the rows x 4 along the weight rows: a wave multiplies MF 16-row fragments
-// (rows 32 f + 16 wm of the tile, so that a tile of fewer rows runs fewer fragments in every
-// wave alike) with 64 weight rows (32 at 32 wn of each half of the weight tile: with SwiGLU
-// the gate rows and their up rows).  K moves in stages of 64 bytes per row through a ring of
-// four LDS buffers (global_load_lds, no registers): stage s + 3 is requested when stage s
-// begins, one barrier per stage.  A row's four 16-byte chunks are stored at chunk
-// c ^ (row / 2 % 4), with which the operand reads run at the LDS's full rate (221 of
-// 256 B/clk measured, 120 without it).
+// BM rows x BN weight rows (SwiGLU: BN / 2 gate and the matching up rows) per workgroup of WM waves
+// along the rows x WN along the weight rows: a wave multiplies MF 16-row fragments (rows
+// 16 (WM f + wm) of the tile, so that a tile of fewer rows runs fewer fragments in every wave
+// alike) with 64 weight rows (32 at 32 wn of each half of the weight tile: with SwiGLU the
+// gate rows and their up rows).  K moves in stages of 128 bytes per row, a whole cache line
+// (with 64 the requests to L2, not its bytes, bound the product), through two LDS buffers
+// (global_load_lds, no registers): stage s + 1 is requested when stage s begins, one barrier
+// per stage.  A row's eight 16-byte chunks are stored at chunk c ^ (row % 8), with which the
+// operand reads run at the LDS's full rate (218 of 256 B/clk measured, 62 without).
 //
-// kBf16: bf16 x bf16, 32 elements per stage.  kFp4: MXFP4 x MXFP4, 128 elements per stage, the
-// four scale bytes of each row's stage in a small ring of their own.  kA16W4: bf16 rows in
-// stages of 32 elements; the weights' codes and scales come in every four stages (64 bytes per
-// row) into a ring of two and become bf16 when a wave reads its fragment.
+// kBf16: bf16 x bf16, 64 elements per stage.  kFp4: MXFP4 x MXFP4, 256 elements per stage.
+// kA16W4: bf16 rows, 64 elements per stage; the weights' codes come in every four stages and
+// become bf16 when a wave reads its fragment.  Scale bytes come in 16 per row at a time: like
+// the operands where every row's scales are 16-byte aligned and K is a multiple of 512
+// (SDMA), else through registers, whose wait also drains the loads on their way.
 
 enum { kBf16 = 0, kA16W4 = 1, kFp4 = 2 };
 
-constexpr int kWideThreads = 512, kWideBM = 256, kWideBN = 256;
-constexpr int kRing = 4;
-constexpr int kTileBytes = 256 * 64;              // one operand's tile of a stage
+template <int WM_, int WN_, int NF_, int MFX_, int PER_CU_>
+struct WideShape {
+  static constexpr int WM = WM_, WN = WN_, NF = NF_, MFX = MFX_;
+  static constexpr int BM = 16 * WM * MFX, BN = 16 * NF * WN, threads = 64 * WM * WN;
+  static constexpr int resident = 256 * PER_CU_;             // workgroups that the chip holds at once
+  static constexpr int waves = PER_CU_ * WM * WN / 4;        // per SIMD
+};
 
+// At most VM loads outstanding, every LDS access done, then the workgroup's barrier.
 template <int VM>
 __device__ __forceinline__ void wait_stage() {
-  // at most VM loads outstanding, every LDS access done, then the workgroup's barrier
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((VM & 15) | (7 << 4) | ((VM >> 4) << 14));
   __builtin_amdgcn_s_barrier();
@@ -369,239 +471,404 @@ __device__ __forceinline__ void wait_stage() {
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 
-// 16 (4) bytes per lane from src into LDS at dst + 16 (4) lane, dst the same for the wave.  Written
-// as an instruction with no register result: the compiler's builtin makes every later LDS read
-// wait for all such loads, those for other ring buffers among them.  The reader's wait is
-// wait_stage's; the compiler's own waits for other loads count these as unknown older or newer
-// ones, which can only make them longer.
-__device__ __forceinline__ void load_lds16(const uint8_t* src, void* dst) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+__device__ __forceinline__ uint32_t lds_offset(void* p) { return (uint32_t)(uintptr_t)(lds_ptr)p; }
+
+// 16 bytes per lane from base + off into LDS at offset dst + 16 lane; base and dst are the same for the
+// wave.  Written as an instruction with no register result: the compiler's builtin makes every
+// later LDS read wait for all such loads, those for the other buffer among them.  The reader's
+// wait is wait_stage's; the compiler's own waits for other loads count these as unknown older or
+// newer ones, which can only make them longer.
+__device__ __forceinline__ void load_lds16(const uint8_t* base, uint32_t off, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(dst), "v"(off), "s"(base)
+               : "memory", "m0");
 }
-__device__ __forceinline__ void load_lds4(const uint8_t* src, void* dst) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)dst);
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(at), "v"(src) : "memory", "m0");
+// The same from an address of the lane's own; 4 bytes per lane.
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(dst), "v"(src) : "memory", "m0");
+}
+__device__ __forceinline__ void load_lds4(const void* src, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, off" ::"s"(dst), "v"(src) : "memory", "m0");
 }
 
-// Four scale bytes of blocks b .. b + 3 of a row of n blocks, at any alignment (blocks past the
-// last count as 2^0).
-__device__ __forceinline__ uint32_t load_scales(const uint8_t* row, int b, int n) {
-  uint32_t v = 0x7F7F7F7Fu;
-  if (b + 4 <= n) {
-    __builtin_memcpy(&v, row + b, 4);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 3; ++i)
-      if (b + i < n) v = (v & ~(0xFFu << (8 * i))) | ((uint32_t)row[b + i] << (8 * i));
+// N (2 or 8) scale bytes of a row of n blocks from block b on, at any alignment (blocks past the last
+// count as 2^0): load() is one load, whose wait comes with value().
+template <int N>
+struct Scales {
+  uint64_t raw;
+  __device__ __forceinline__ void load(const uint8_t* row, int b, int n) {   // n >= N
+    raw = 0;
+    __builtin_memcpy(&raw, row + min(b, n - N), N);
   }
-  return v;
-}
-
-struct WideLds {
-  uint8_t x[kRing][kTileBytes];
-  uint8_t w[kRing][kTileBytes];
-  uint32_t s[kRing][512];                         // scales: weight rows, then rows (MXFP4)
-};
-struct WideLdsBf16 {
-  uint8_t x[kRing][kTileBytes];
-  uint8_t w[kRing][kTileBytes];
-};
-struct WideLdsA16 {
-  uint8_t x[kRing][kTileBytes];
-  uint8_t w[2][kTileBytes];
-  uint32_t s[2][256];
-};
-template <int MODE> struct WideLdsOf { typedef WideLds type; };
-template <> struct WideLdsOf<kBf16> { typedef WideLdsBf16 type; };
-template <> struct WideLdsOf<kA16W4> { typedef WideLdsA16 type; };
-
-// SDMA: the scales of a row start at a multiple of four bytes and K is a multiple of 128, so they
-// go straight into LDS like the operands; otherwise they pass through a register, whose wait
-// also drains the loads on their way.
-template <int MODE, bool SDMA, int MF>
-__device__ __forceinline__ void wide_tile(const ProductArgs& a, const Tile& t, typename WideLdsOf<MODE>::type& lds) {
-  constexpr int XQ = MF > 4 ? 2 : 1;              // x loads per thread and stage: 128 rows each
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
-  const int wm = wave & 1, wn = wave >> 1;
-  const int n_out = a.swiglu ? a.N / 2 : a.N;
-  const int c0 = t.nb * (a.swiglu ? kWideBN / 2 : kWideBN);
-  const int64_t K = a.K;
-  const int64_t wrow_b = MODE == kBf16 ? 2 * K : K / 2, xrow_b = MODE == kFp4 ? K / 2 : 2 * a.ldx;
-  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;   // bytes of a row in use
-  const int stages = (xb + 63) / 64;
-
-  // this thread's 16 bytes of a stage: rows tid / 4 and 128 + tid / 4, logical chunk ch
-  const int ch = (tid & 3) ^ ((tid >> 3) & 3);
-  const uint8_t *wp[2], *xp[2];
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int row = a.swiglu ? min(c0 + (tid >> 2), n_out - 1) + q * n_out : min(c0 + q * 128 + (tid >> 2), n_out - 1);
-    wp[q] = a.w + ((int64_t)t.entry * a.N + row) * wrow_b + ch * 16;
-    const int i = t.row0 + min(q * 128 + (tid >> 2), t.nrows - 1);
-    xp[q] = a.x + (int64_t)max(x_row(a, i, a.perm ? a.perm[i] : i), 0) * xrow_b + ch * 16;
+  __device__ __forceinline__ uint64_t value(int b, int n) const {
+    const uint64_t none = 0x7F7F7F7F7F7F7F7Full;
+    const int d = b - min(b, n - N);              // bytes that were read too early
+    return d == 0 ? raw : d >= N ? none : (raw >> (8 * d)) | (none << (8 * (N - d)));
   }
-  const uint8_t* sp = nullptr;                    // scales of weight row tid, and of row tid - 256
-  if (MODE != kBf16) {
-    if (tid < 256) {
-      const int r = tid & 127, q = tid >> 7;
-      const int row = a.swiglu ? min(c0 + r, n_out - 1) + q * n_out : min(c0 + tid, n_out - 1);
-      sp = a.ws + ((int64_t)t.entry * a.N + row) * (K / 32);
-    } else if (MODE == kFp4) {
-      const int i = t.row0 + min(tid - 256, t.nrows - 1);
-      sp = a.xs + (int64_t)max(x_row(a, i, a.perm ? a.perm[i] : i), 0) * (K / 32);
+  // the first N bytes of a row of any length
+  __device__ __forceinline__ static uint64_t first(const uint8_t* row, int n) {
+    uint64_t v = 0x7F7F7F7F7F7F7F7Full;
+    if (n >= N) {
+      __builtin_memcpy(&v, row, N);
+    } else {
+      for (int i = 0; i < n; ++i) v = (v & ~(0xFFull << (8 * i))) | ((uint64_t)row[i] << (8 * i));
     }
+    return v;
   }
-  const int nblk = a.K / 32;
-  uint32_t sc = 0;
-  // 64 bytes of every weight row and the scales of their blocks: stage s (kA16W4: four stages)
-  auto request_w = [&](int s) {
-    const int b = MODE == kA16W4 ? s & 1 : s & (kRing - 1);
-    // a chunk past the row's end (only in the last stage) re-reads the row's first bytes
-    const int64_t off = s * 64 + ch * 16 < wb ? (int64_t)s * 64 : -(int64_t)(ch * 16);
-    if constexpr (MODE != kBf16) {
-      if (MODE == kFp4 || wave < 4) {
-        if (SDMA) load_lds4(sp + s * 4, &lds.s[b][wave * 64]);
-        else sc = load_scales(sp, s * 4, nblk);
+};
+
+template <int MODE, class S>
+struct WideLds {
+  uint8_t x[2][S::BM * 128];
+  uint8_t w[2][S::BN * 128];
+  // scales of the weight rows, then (MXFP4) of the rows, 16 bytes each
+  uint8_t s[MODE == kBf16 ? 1 : 2][MODE == kBf16 ? 16 : (S::BN + (MODE == kFp4 ? S::BM : 0)) * 16];
+  int perm[S::BM];                                // routes of the next tile's rows
+  int first[kMaxGroups + 1];
+};
+
+// What a thread loads of a tile: its 16 bytes of every stage, of rows tid / 8 + RQ q, and the scales
+// of one row.
+template <int MODE, class S>
+struct WideSource {
+  static constexpr int T = S::threads, RQ = T / 8, WQ = S::BN / RQ, XQ = S::BM / RQ;
+  static constexpr int SR = MODE == kBf16 ? 0 : S::BN + (MODE == kFp4 ? S::BM : 0);
+  static constexpr int SQ = SR == 0 ? 1 : div_up(SR, T);      // rows of scales per thread: tid + T q
+  // offsets (32 bits: launch_wide checks that a matrix and all of x are that small) from the group's
+  // matrix and from x; the scales' address
+  const uint8_t *wbase, *s[SQ];
+  uint32_t w[WQ], x[XQ];
+
+  // perm: the routes of the tile's rows (any pointer; unused without a.perm).
+  template <class P>
+  __device__ __forceinline__ void point(const ProductArgs& a, const Tile& t, int ch, P perm) {
+    constexpr int HN = S::BN / 2;
+    const int tid = threadIdx.x;
+    auto x_at = [&](int r) {
+      const int m = min(r, t.nrows - 1), i = t.row0 + m;
+      return max(x_row(a, i, a.perm ? perm[m] : i), 0);
+    };
+    const int n_out = a.swiglu ? a.N / 2 : a.N, c0 = t.nb * (a.swiglu ? HN : S::BN);
+    const int64_t K = a.K;
+    const uint32_t wrow_b = MODE == kBf16 ? 2 * a.K : a.K / 2, xrow_b = MODE == kFp4 ? a.K / 2 : 2 * (uint32_t)a.ldx;
+    auto w_row = [&](int r) {
+      return a.swiglu ? min(c0 + r % HN, n_out - 1) + (r >= HN ? n_out : 0) : min(c0 + r, n_out - 1);
+    };
+    wbase = a.w + (int64_t)t.entry * a.N * wrow_b;
+#pragma unroll
+    for (int q = 0; q < WQ; ++q) w[q] = w_row(q * RQ + (tid >> 3)) * wrow_b + ch * 16;
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) x[q] = x_at(q * RQ + (tid >> 3)) * xrow_b + ch * 16;
+    if (MODE != kBf16) {
+#pragma unroll
+      for (int q = 0; q < SQ; ++q) {
+        const int r = q * T + tid;
+        if (MODE == kFp4 && r >= S::BN) s[q] = a.xs + (int64_t)x_at(r - S::BN) * (K / 32);
+        else s[q] = a.ws + ((int64_t)t.entry * a.N + w_row(min(r, S::BN - 1))) * (K / 32);
       }
     }
+  }
+};
+
+// Buffers that the stages, the weights (kA16W4: every four stages) and the scales of a tile begin in.
+struct WideTurn {
+  int stage, w, s;
+};
+
+template <int MODE, class S, bool SDMA, int MF>
+__device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLds<MODE, S>& lds, const Tile& t,
+                                          WideSource<MODE, S>& src, WideTurn& turn, Scales<MODE == kFp4 ? 8 : 2>* sc,
+                                          bool more, int b, int total, Tile& next, uint32_t wdst, uint32_t xdst,
+                                          uint32_t sdst) {
+  constexpr int WM = S::WM, HN = S::BN / 2, T = S::threads, RQ = T / 8;
+  constexpr int WQ = S::BN / RQ, XQ = (MF * 16 * WM + RQ - 1) / RQ;
+  constexpr int SR = WideSource<MODE, S>::SR, SQ = WideSource<MODE, S>::SQ, NF = S::NF;
+  constexpr int period = MODE == kFp4 ? 2 : 8;               // stages that one load of scales covers
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+  const int wm = wave % WM, wn = wave / WM;
+  const int n_out = a.swiglu ? a.N / 2 : a.N;
+  const int c0 = t.nb * (a.swiglu ? HN : S::BN);
+  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;   // bytes of a row in use
+  const int stages = (xb + 127) / 128;
+  const int nblk = a.K / 32;
+  const int ch = (tid & 7) ^ ((tid >> 3) & 7);
+  const uint32_t pdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.perm[0]) + wave * 256);
+
+  // Scales of period p straight into LDS; or of stage s, in two steps through a register.
+  auto request_scales = [&](int p, int at) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) load_lds16(wp[q] + off, &lds.w[b][q * 8192 + wave * 1024]);
+    for (int q = 0; q < SQ; ++q)
+      if (SR % T == 0 || q * T + wave * 64 < SR)
+        load_lds16(src.s[q] + p * 16, sdst + ((p + at) & 1) * sizeof(lds.s[0]) + q * T * 16);
   };
-  auto request_x = [&](int s) {
-    const int b = s & (kRing - 1);
-    const int64_t off = s * 64 + ch * 16 < xb ? (int64_t)s * 64 : -(int64_t)(ch * 16);
+  constexpr int SN = MODE == kFp4 ? 8 : 2;
+  auto put_scales = [&](int s, int q, uint64_t v) {
+    if (SR % T == 0 || q * T + tid < SR) __builtin_memcpy(&lds.s[(s + turn.stage) & 1][(q * T + tid) * 16], &v, SN);
+  };
+  // Stage s: 128 bytes of every weight row (kA16W4: four stages of x), of every row of x; a chunk past
+  // the row's end (only in the last stage) re-reads the row's first bytes.
+  auto request_w = [&](int s, int at) {
+    const uint32_t dst = wdst + ((s + at) & 1) * S::BN * 128;
+    if ((s + 1) * 128 <= wb) {
 #pragma unroll
-    for (int q = 0; q < XQ; ++q) load_lds16(xp[q] + off, &lds.x[b][q * 8192 + wave * 1024]);
-  };
-  auto put_scales = [&](int s) {
-    if constexpr (MODE != kBf16 && !SDMA) {
-      if (MODE == kFp4 || wave < 4) lds.s[MODE == kA16W4 ? s & 1 : s & (kRing - 1)][tid] = sc;
+      for (int q = 0; q < WQ; ++q) load_lds16(src.wbase + s * 128, src.w[q], dst + q * RQ * 128);
+    } else {
+      const uint32_t off = s * 128 + ch * 16 < wb ? s * 128 : -(uint32_t)(ch * 16);
+#pragma unroll
+      for (int q = 0; q < WQ; ++q) load_lds16(src.wbase, src.w[q] + off, dst + q * RQ * 128);
     }
   };
+  auto request_x = [&](int s, int at, int q) {
+    const uint32_t dst = xdst + (((s + at) & 1) * S::BM + q * RQ) * 128;
+    if ((s + 1) * 128 <= xb)
+      load_lds16(a.x + s * 128, src.x[q], dst);
+    else
+      load_lds16(a.x, src.x[q] + (s * 128 + ch * 16 < xb ? s * 128 : -(uint32_t)(ch * 16)), dst);
+  };
 
-  f32x4_t acc[4][MF];
+  f32x4_t acc[NF][MF];
 #pragma unroll
-  for (int f = 0; f < 4; ++f)
+  for (int f = 0; f < NF; ++f)
 #pragma unroll
     for (int m = 0; m < MF; ++m) acc[f][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  const int swz = (l16 >> 1) & 3;
-  const int frag = l16 * 64 + ((g ^ swz) << 4);
-  const int xfrag = wm * 16 * 64 + frag;
-  auto compute = [&](int s) {
-    const int b = s & (kRing - 1);
-    u32x4_t w[4];
-    uint32_t sw[4];
-#pragma unroll
-    for (int f = 0; f < 4; ++f) {
-      const int row = (f >> 1) * 128 + (f & 1) * 16 + wn * 32;
+  const int swz = l16 & 7;
+  // The products of stage s: two halves of 64 bytes (the second missing where the row ends), of each
+  // NF weight fragments x MF row fragments.  The next row fragment is read from LDS, and a weight
+  // fragment of the second half, ahead of each row fragment's products; left free, the scheduler
+  // sinks every read to its use, with its latency in between.
+  auto compute = [&](int s, bool two) {
+    // buffer and place of the stage's scales
+    const int sb = (SDMA ? s / period + turn.s : s + turn.stage) & 1, so = SDMA ? s % period * SN : 0;
+    const int b = (s + turn.stage) & 1;
+    const int at[2] = {l16 * 128 + ((g ^ swz) << 4), l16 * 128 + (((4 + g) ^ swz) << 4)};
+    u32x4_t w[2][NF], x[2];
+    uint32_t sw[2][NF], sx[2];
+    auto read_w = [&](int kk, int f) {
+      const int row = f / (NF / 2) * HN + f % (NF / 2) * 16 + wn * (8 * NF);
       if constexpr (MODE == kA16W4) {
-        // element 8 g of block s of the row: a dword of its 16-byte chunk
-        const int c = (s >> 2) & 1, j = s & 3;
-        const uint32_t code =
-            *reinterpret_cast<const uint32_t*>(&lds.w[c][(row + l16) * 64 + ((j ^ swz) << 4) + g * 4]);
-        const uint32_t X = reinterpret_cast<const uint8_t*>(lds.s[c])[(row + l16) * 4 + j];
-        w[f] = __builtin_bit_cast(u32x4_t, fp4x8_bf16(code, e8m0_or_nan(X)));
+        // elements 8 g .. 8 g + 7 of a block: one dword of its chunk
+        const int c = ((s >> 2) + turn.w) & 1, j = (s & 3) * 2 + kk;
+        w[kk][f][0] = *reinterpret_cast<const uint32_t*>(&lds.w[c][(row + l16) * 128 + ((j ^ swz) << 4) + g * 4]);
+        sw[kk][f] = lds.s[sb][(row + l16) * 16 + so + kk];
       } else {
-        w[f] = *reinterpret_cast<const u32x4_t*>(&lds.w[b][row * 64 + frag]);
-        if constexpr (MODE == kFp4) sw[f] = lds.s[b][row + l16] >> (8 * g);
+        w[kk][f] = *reinterpret_cast<const u32x4_t*>(&lds.w[b][row * 128 + at[kk]]);
+        if constexpr (MODE == kFp4)
+          sw[kk][f] = *reinterpret_cast<const uint32_t*>(&lds.s[sb][(row + l16) * 16 + so + kk * 4]);
       }
-    }
+    };
+    auto read_x = [&](int kk, int m) {
+      const int row = (m * WM + wm) * 16;
+      x[m & 1] = *reinterpret_cast<const u32x4_t*>(&lds.x[b][row * 128 + at[kk]]);
+      if constexpr (MODE == kFp4)
+        sx[m & 1] = *reinterpret_cast<const uint32_t*>(&lds.s[sb][(S::BN + row + l16) * 16 + so + kk * 4]);
+    };
+    auto half = [&](auto k) {
+      constexpr int kk = decltype(k)::value;
 #pragma unroll
-    for (int m = 0; m < MF; ++m) {
-      const u32x4_t x = *reinterpret_cast<const u32x4_t*>(&lds.x[b][xfrag + m * 32 * 64]);
-      if constexpr (MODE == kFp4) {
-        const uint32_t sx = lds.s[b][256 + m * 32 + wm * 16 + l16] >> (8 * g);
-#pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f][m] = mfma_fp4(w[f], sw[f], x, sx, acc[f][m]);
-      } else {
-#pragma unroll
-        for (int f = 0; f < 4; ++f) acc[f][m] = mfma_bf16(w[f], x, acc[f][m]);
+      for (int f = 0; f < NF; ++f) {
+        if constexpr (MODE == kA16W4)
+          w[kk][f] = __builtin_bit_cast(u32x4_t, fp4x8_bf16(w[kk][f][0], e8m0_or_nan(sw[kk][f])));
+        else if constexpr (MODE == kFp4)
+          sw[kk][f] >>= 8 * g;
       }
+#pragma unroll
+      for (int m = 0; m < MF; ++m) {
+        if (m + 1 < MF) read_x(kk, m + 1);
+        if (kk == 0) {
+#pragma unroll
+          for (int f = m * NF / MF; f < (m + 1) * NF / MF; ++f) read_w(1, f);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        const uint32_t sxm = MODE == kFp4 ? sx[m & 1] >> (8 * g) : 0;
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          if constexpr (MODE == kFp4) acc[f][m] = mfma_fp4(w[kk][f], sw[kk][f], x[m & 1], sxm, acc[f][m]);
+          else acc[f][m] = mfma_bf16(w[kk][f], x[m & 1], acc[f][m]);
+        }
+      }
+    };
+#pragma unroll
+    for (int f = 0; f < NF; ++f) read_w(0, f);
+    read_x(0, 0);
+    half(Const<0>());
+    if (two) {
+      read_x(1, 0);
+      half(Const<1>());
     }
   };
 
-  if (MODE == kA16W4) {
-    request_w(0);
-    put_scales(0);
-  }
-  for (int s = 0; s < kRing - 1 && s < stages; ++s) {
-    if (MODE != kA16W4) {
-      request_w(s);
-      put_scales(s);
-    }
-    request_x(s);
-  }
-  int s = 0;
-  for (; s + kRing - 1 < stages; ++s) {
-    // stage s is in; s + 1 and s + 2 (and with s % 4 = 1, 2 the weights of the next four stages,
-    // requested with or after stage s + 1) may be on their way
-    if (MODE != kA16W4) wait_stage<2 * (2 + XQ + (MODE == kFp4 && SDMA))>();
-    else if (((s - 1) & 3) < 2) wait_stage<2 * XQ + 2>();
-    else wait_stage<2 * XQ>();
-    if (MODE != kA16W4) request_w(s + kRing - 1);
-    else if ((s & 3) == 0 && (s + 4) < stages) request_w((s >> 2) + 1);
-    request_x(s + kRing - 1);
-    compute(s);
-    if (MODE != kA16W4) put_scales(s + kRing - 1);
-    else if ((s & 3) == 0 && (s + 4) < stages) put_scales((s >> 2) + 1);
-  }
-  for (; s < stages; ++s) {
-    if (MODE == kFp4 && !SDMA && s + 1 == stages && (xb & 63)) {
-      // the last stage's chunks past the row's end count as zeros: of one operand, since every
-      // e2m1 code is finite
-      __builtin_amdgcn_s_waitcnt(0 | (7 << 4) | (15 << 8));
+  for (int s = 0; s < stages; ++s) {
+    const bool last = s + 1 == stages;
+    if (MODE == kFp4 && last && (xb & 127)) {
+      // chunks past the row's end count as zeros: of one operand, since every e2m1 code is finite
+      __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
       asm volatile("" ::: "memory");
-      if (s * 64 + ch * 16 >= wb) {
+      if (s * 128 + ch * 16 >= wb) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-          *reinterpret_cast<u32x4_t*>(&lds.w[s & (kRing - 1)][q * 8192 + tid * 16]) = u32x4_t{0, 0, 0, 0};
+        for (int q = 0; q < WQ; ++q)
+          *reinterpret_cast<u32x4_t*>(&lds.w[(s + turn.stage) & 1][q * RQ * 128 + tid * 16]) = u32x4_t{0, 0, 0, 0};
       }
     }
-    wait_stage<0>();
-    compute(s);
+    // stage s is in; of a tile's first stage every wave has made sure before it stored the last
+    // tile's results, which may still be on their way
+    if (s == 0) wait_stage<63>();
+    else wait_stage<0>();
+    if (!last) {
+      if (MODE != kBf16 && !SDMA) {
+#pragma unroll
+        for (int q = 0; q < SQ; ++q) {
+          put_scales(s + 1, q, sc[q].value((s + 1) * SN, nblk));
+          sc[q].load(src.s[q], (s + 2) * SN, nblk);
+        }
+      }
+      if (MODE == kFp4 && SDMA && (s + 1) % period == 0) request_scales((s + 1) / period, turn.s);
+      if (MODE == kA16W4 && (s & 3) == 0 && s + 4 < stages) {
+        if (SDMA && (s & 7) == 4) request_scales((s >> 3) + 1, turn.s);
+        request_w((s >> 2) + 1, turn.w);
+      }
+      if (MODE != kA16W4) request_w(s + 1, turn.stage);
+#pragma unroll
+      for (int q = 0; q < XQ; ++q) request_x(s + 1, turn.stage, q);
+    }
+    // The workgroup's next tile: looked up while the first stage is computed, its first stage
+    // requested while the last one is.  No vector load into registers here: the compiler would
+    // wait for it, and so for the stage on its way, before this stage's products.
+    if (s == 0 && more) {
+      next_tile<S::BM>(a, b, total, n_nb, lds.first, &next);
+      if (a.perm && wave * 64 < S::BM)
+        load_lds4(a.perm + next.row0 + min(tid, next.nrows - 1), pdst);
+    }
+    if (last && more) {
+      if (stages == 1) wait_stage<0>();
+      src.point(a, next, ch, lds.perm);
+      const int sn = turn.stage + stages;
+      if (MODE != kBf16 && SDMA) request_scales(0, turn.s + (stages + period - 1) / period);
+      request_w(0, MODE == kA16W4 ? turn.w + (stages + 3) / 4 : sn);
+#pragma unroll
+      for (int q = 0; q < S::BM / RQ; ++q)
+        if (q * RQ < next.nrows) request_x(0, sn, q);
+    }
+    compute(s, MODE == kFp4 || s * 128 + 64 < xb);
+  }
+  turn.stage += stages;
+  turn.s += (stages + period - 1) / period;
+  turn.w += (stages + 3) / 4;
+  if (MODE != kBf16 && !SDMA && more) {
+#pragma unroll
+    for (int q = 0; q < SQ; ++q) {
+      put_scales(0, q, Scales<SN>::first(src.s[q], nblk));
+      if (stages > 1) sc[q].load(src.s[q], SN, nblk);
+    }
   }
 
+  int row[MF];
+  bool on[MF];
   RowOut o[MF];
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
-    const int r = m * 32 + wm * 16 + l16;
-    o[m] = row_out(a, t.row0 + min(r, t.nrows - 1), r < t.nrows);
+    const int r = (m * WM + wm) * 16 + l16;
+    row[m] = t.row0 + min(r, t.nrows - 1);
+    on[m] = r < t.nrows;
   }
+  rows_out<MF>(a, row, on, o);
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));          // the next tile's first stage
+  asm volatile("" ::: "memory");
+  with_format(a, [&](auto yf, auto vec) {
+    constexpr int YF = decltype(yf)::value;
+    constexpr bool VEC = decltype(vec)::value;
 #pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    if (a.swiglu) {
-      store_pair(a, o[m], c0 + wn * 32, n_out, swiglu4(acc[0][m], acc[2][m]), swiglu4(acc[1][m], acc[3][m]));
-    } else {
-      store_pair(a, o[m], c0 + wn * 32, n_out, acc[0][m], acc[1][m]);
-      store_pair(a, o[m], c0 + 128 + wn * 32, n_out, acc[2][m], acc[3][m]);
+    for (int m = 0; m < MF; ++m) {
+      const int col = c0 + wn * (8 * NF);
+#pragma unroll
+      for (int f = 0; f < NF / 2; f += 2) {
+        if (a.swiglu) {
+          store_pair<YF, VEC>(a, o[m], col + f * 16, n_out, swiglu4(acc[f][m], acc[NF / 2 + f][m]),
+                              swiglu4(acc[f + 1][m], acc[NF / 2 + f + 1][m]));
+        } else {
+          store_pair<YF, VEC>(a, o[m], col + f * 16, n_out, acc[f][m], acc[f + 1][m]);
+          store_pair<YF, VEC>(a, o[m], col + HN + f * 16, n_out, acc[NF / 2 + f][m], acc[NF / 2 + f + 1][m]);
+        }
+      }
     }
-  }
+  });
 }
 
-template <int MODE, bool SDMA>
-__global__ void __launch_bounds__(kWideThreads, 2)
+// A workgroup takes tiles blockIdx.x, blockIdx.x + gridDim.x, ... (the grid is as large as the chip
+// holds at once): the first stage of its next tile arrives while it finishes the last one.
+template <int MODE, class S, bool SDMA>
+__global__ void __launch_bounds__(S::threads, S::waves)
 product_wide_kernel(ProductArgs a, int n_nb) {
-  __shared__ __attribute__((aligned(16))) typename WideLdsOf<MODE>::type lds;
-  Tile t;
-  if (!find_tile<kWideBM, true>(a, blockIdx.x, n_nb, &t)) return;
-  // 32-row steps of the tile, the same for the whole workgroup
-  const int steps = (t.nrows + 31) >> 5;
-  if constexpr (SDMA) {
-    switch (steps) {
-      case 1: wide_tile<MODE, SDMA, 1>(a, t, lds); break;
-      case 2: wide_tile<MODE, SDMA, 2>(a, t, lds); break;
-      case 3: wide_tile<MODE, SDMA, 3>(a, t, lds); break;
-      case 4: wide_tile<MODE, SDMA, 4>(a, t, lds); break;
-      case 5: wide_tile<MODE, SDMA, 5>(a, t, lds); break;
-      case 6: wide_tile<MODE, SDMA, 6>(a, t, lds); break;
-      case 7: wide_tile<MODE, SDMA, 7>(a, t, lds); break;
-      default: wide_tile<MODE, SDMA, 8>(a, t, lds); break;
-    }
+  __shared__ __attribute__((aligned(16))) WideLds<MODE, S> lds;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  int total;
+  if (a.offsets) {
+    if (wave == 0) first_tiles<S::BM>(a, lds.first);
+    __syncthreads();
+    total = __builtin_amdgcn_readfirstlane(lds.first[a.E]) * n_nb;
   } else {
-    if (steps <= 2) wide_tile<MODE, SDMA, 2>(a, t, lds);
-    else if (steps <= 4) wide_tile<MODE, SDMA, 4>(a, t, lds);
-    else wide_tile<MODE, SDMA, 8>(a, t, lds);
+    total = div_up(a.M, S::BM) * n_nb;
+  }
+  int b = blockIdx.x;
+  if (b >= total) return;
+  Tile t;
+  next_tile<S::BM>(a, b, total, n_nb, lds.first, &t);
+  WideSource<MODE, S> src;
+  const int ch = (tid & 7) ^ ((tid >> 3) & 7);
+  src.point(a, t, ch, a.perm + t.row0);
+  const uint32_t wdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.w[0][wave * 1024]));
+  const uint32_t xdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.x[0][wave * 1024]));
+  const uint32_t sdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.s[0][0]) + wave * 1024);
+  // the first tile's first stage
+  constexpr int T = S::threads, RQ = T / 8, SR = WideSource<MODE, S>::SR, SQ = WideSource<MODE, S>::SQ;
+  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;
+  constexpr int SN = MODE == kFp4 ? 8 : 2;
+  Scales<SN> sc[SQ] = {};
+  if (MODE != kBf16) {
+#pragma unroll
+    for (int q = 0; q < SQ; ++q) {
+      if (SDMA) {
+        if (SR % T == 0 || q * T + wave * 64 < SR) load_lds16(src.s[q], sdst + q * T * 16);
+      } else {
+        const uint64_t v = Scales<SN>::first(src.s[q], a.K / 32);
+        if (SR % T == 0 || q * T + tid < SR) __builtin_memcpy(&lds.s[0][(q * T + tid) * 16], &v, SN);
+        if (xb > 128) sc[q].load(src.s[q], SN, a.K / 32);
+      }
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < S::BN / RQ; ++q) load_lds16(src.wbase, src.w[q] - (ch * 16 < wb ? 0 : ch * 16), wdst + q * RQ * 128);
+#pragma unroll
+  for (int q = 0; q < S::BM / RQ; ++q)
+    if (q * RQ < t.nrows) load_lds16(a.x, src.x[q] - (ch * 16 < xb ? 0 : ch * 16), xdst + q * RQ * 128);
+  __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
+  asm volatile("" ::: "memory");
+
+  WideTurn turn{0, 0, 0};
+  for (;;) {
+    b += gridDim.x;
+    const bool more = b < total;
+    Tile next = t;
+    // fragments that the tile's rows need of every wave, the same for the whole workgroup
+    const int steps = div_up(t.nrows, 16 * S::WM);
+    auto run = [&](auto mf) {
+      wide_tile<MODE, S, SDMA, decltype(mf)::value>(a, n_nb, lds, t, src, turn, sc, more, b, total, next, wdst, xdst, sdst);
+    };
+    if constexpr (!SDMA) {
+      if (2 * steps <= S::MFX) run(Const<S::MFX / 2>());
+      else run(Const<S::MFX>());
+    } else if (S::MFX > 4 && steps > 4) {
+      if (steps == 8) run(Const<S::MFX>());
+      else if (steps == 7) run(Const<S::MFX - S::MFX / 8>());
+      else if (steps == 6) run(Const<S::MFX - S::MFX / 4>());
+      else run(Const<S::MFX / 2 + S::MFX / 8>());
+    } else {
+      if (steps == 4) run(Const<4>());
+      else if (steps == 3) run(Const<3>());
+      else if (steps == 2) run(Const<2>());
+      else run(Const<1>());
+    }
+    if (!more) return;
+    t = next;
   }
 }
 
@@ -664,7 +931,7 @@ static int launch_few(const ProductArgs& a, hipStream_t s) {
   const int64_t n_nb = (n_out + cols - 1) / cols;
   const int mf = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
   const int64_t tiles = most_row_tiles(a, 16 * mf) * n_nb;
-  MC_REQUIRE(tiles <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
+  MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   const int steps = WF == MC_BF16 ? a.K / 32 : (a.K + 127) / 128;
   const unsigned grid = (unsigned)tiles;
   if (nt == 4) {
@@ -680,26 +947,43 @@ static int launch_few(const ProductArgs& a, hipStream_t s) {
   return MC_OK;
 }
 
+template <class S>
 static int launch_wide(const ProductArgs& a, hipStream_t s) {
-  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? kWideBN / 2 : kWideBN;
-  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, kWideBM) * n_nb;
-  MC_REQUIRE(tiles <= 0x7FFFFFFF, "product of %d rows with %d columns is too large", a.M, a.N);
-  const bool sdma = a.K % 128 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 4 == 0;
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? S::BN / 2 : S::BN;
+  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, S::BM) * n_nb;
+  MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   auto run = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(kWideThreads), 0, s, a, (int)n_nb);
+    const int64_t grid = tiles < S::resident ? tiles : S::resident;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::threads), 0, s, a, (int)n_nb);
   };
-  if (a.w_fmt == MC_BF16) run(product_wide_kernel<kBf16, true>);
-  else if (a.x_fmt == MC_BF16 && sdma) run(product_wide_kernel<kA16W4, true>);
-  else if (a.x_fmt == MC_BF16) run(product_wide_kernel<kA16W4, false>);
-  else if (sdma) run(product_wide_kernel<kFp4, true>);
-  else run(product_wide_kernel<kFp4, false>);
+  const bool sdma = a.K % 512 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 16 == 0;
+  if (a.w_fmt == MC_BF16) run(product_wide_kernel<kBf16, S, true>);
+  else if (a.x_fmt == MC_BF16 && sdma) run(product_wide_kernel<kA16W4, S, true>);
+  else if (a.x_fmt == MC_BF16) run(product_wide_kernel<kA16W4, S, false>);
+  else if (sdma) run(product_wide_kernel<kFp4, S, true>);
+  else run(product_wide_kernel<kFp4, S, false>);
   MC_LAUNCH_CHECK();
   return MC_OK;
 }
 
 int launch_product(const ProductArgs& a, hipStream_t s) {
   if (a.M == 0 || a.N == 0 || a.x_rows == 0 || a.y_rows == 0 || a.n == 0) return MC_OK;
-  if (a.M > 64) return launch_wide(a, s);
+  typedef WideShape<2, 4, 4, 8, 1> Big;           // 256 x 256, one workgroup per CU
+  typedef WideShape<2, 2, 4, 4, 2> Medium;        // 128 x 128, two per CU
+  // bytes of a matrix and of x, which the wide kernels reach with 32-bit offsets
+  const int64_t w_bytes = (int64_t)a.N * (a.w_fmt == MC_BF16 ? 2 * (int64_t)a.K : a.K / 2);
+  const int64_t x_bytes = a.x_rows * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
+  if (a.M > 64 && w_bytes <= UINT32_MAX && x_bytes <= UINT32_MAX) {
+    // The large tiles read each operand half as often, and win where they fill the chip with full
+    // tiles: 8192 x 4096 x 4096 in fp4 86 against 101 us, 256 experts of 192 rows 1.40 against
+    // 1.68 ms a layer.  Where groups are small or uneven the small ones win: 24 rows a group 268
+    // against 276 us, 64 groups of 250 rows on average, skewed, 207 against 231 us.
+    const int64_t groups = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
+    const int64_t cols = a.swiglu ? Big::BN / 2 : Big::BN, n_nb = ((a.swiglu ? a.N / 2 : a.N) + cols - 1) / cols;
+    const int64_t tiles = (a.offsets ? a.M / Big::BM + groups / 2 : (a.M + Big::BM - 1) / Big::BM) * n_nb;
+    if (a.M / groups >= 128 && tiles >= (a.offsets ? 1024 : 192)) return launch_wide<Big>(a, s);
+    return launch_wide<Medium>(a, s);
+  }
   if (a.x_fmt == MC_MXFP4) return launch_few<MC_MXFP4, MC_MXFP4>(a, s);
   if (a.w_fmt == MC_MXFP4) return launch_few<MC_BF16, MC_MXFP4>(a, s);
   return launch_few<MC_BF16, MC_BF16>(a, s);
