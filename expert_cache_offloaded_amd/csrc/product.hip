@@ -307,8 +307,8 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t w, uint32_t sw, u32x4_t x, u
 
 // ---------------------------------------------------------------- few rows
 //
-// Tiles of 16 MF rows x 16 NT weight rows (SwiGLU: NT / 2 fragments of gate rows and the matching
-// up rows), NT x KW waves: a wave multiplies one 16-row weight fragment over every KW-th
+// Tiles of 16 rows x 16 NT weight rows (SwiGLU: NT / 2 fragments of gate rows and the matching up
+// rows), NT x KW waves: a wave multiplies one 16-row weight fragment over every KW-th
 // step of K (64 bytes of each weight row per step), operands straight from memory, and the KW
 // partial sums meet in LDS in a fixed order.  With few rows the weights are read once and bound
 // the product; what counts is that all of a wave's loads are on their way at once (kFewSteps steps
@@ -317,12 +317,12 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t w, uint32_t sw, u32x4_t x, u
 
 constexpr int kFewSteps = 4;
 
-template <int XF, int WF, int MF, int NT, int KW>
+template <int XF, int WF, int NT, int KW>
 __global__ void __launch_bounds__(64 * NT * KW)
 product_few_kernel(ProductArgs a, int n_nb) {
-  __shared__ f32x4_t part[KW][NT][MF][64];
+  __shared__ f32x4_t part[KW][NT][64];
   Tile t;
-  if (!find_tile<16 * MF>(a, blockIdx.x, n_nb, &t)) return;
+  if (!find_tile<16>(a, blockIdx.x, n_nb, &t)) return;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int f = wave % NT, kw = wave / NT;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
@@ -335,19 +335,12 @@ product_few_kernel(ProductArgs a, int n_nb) {
                             : min(c0 + f * 16 + l16, n_out - 1);
   const uint8_t* wp = a.w + ((int64_t)t.entry * a.N + wrow) * wrow_b;
   const uint8_t* wsp = a.ws + ((int64_t)t.entry * a.N + wrow) * (K / 32);
-  const uint8_t* xp[MF];
-  const uint8_t* xsp[MF];
-#pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    const int i = t.row0 + min(16 * m + l16, t.nrows - 1);
-    const int64_t xr = max(x_row(a, i, a.perm ? a.perm[i] : i), 0);
-    xp[m] = a.x + xr * xrow_b;
-    xsp[m] = a.xs + xr * (K / 32);
-  }
+  const int i_row = t.row0 + min(l16, t.nrows - 1);
+  const int64_t xr = max(x_row(a, i_row, a.perm ? a.perm[i_row] : i_row), 0);
+  const uint8_t* xp = a.x + xr * xrow_b;
+  const uint8_t* xsp = a.xs + xr * (K / 32);
 
-  f32x4_t acc[MF];
-#pragma unroll
-  for (int m = 0; m < MF; ++m) acc[m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
   for (int s0 = kw; s0 < steps; s0 += KW * kFewSteps) {
     u32x4_t w[kFewSteps];
     uint32_t sw[kFewSteps];
@@ -370,66 +363,49 @@ product_few_kernel(ProductArgs a, int n_nb) {
       const int b = WF == MC_BF16 ? s : min(4 * s + g, nblk - 1);
       if (!in) w[u] = u32x4_t{0, 0, 0, 0};
       if (WF == MC_BF16) {
-#pragma unroll
-        for (int m = 0; m < MF; ++m) {
-          u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 64 + 16 * g);
-          if (!in) x = u32x4_t{0, 0, 0, 0};       // a zero times an infinity is no zero
-          acc[m] = mfma_bf16(w[u], x, acc[m]);
-        }
+        u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp + (int64_t)b * 64 + 16 * g);
+        if (!in) x = u32x4_t{0, 0, 0, 0};         // a zero times an infinity is no zero
+        acc = mfma_bf16(w[u], x, acc);
       } else if (XF == MC_MXFP4) {
-        if (!in) sw[u] = 127u;
-#pragma unroll
-        for (int m = 0; m < MF; ++m) {
-          const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 16);
-          const uint32_t sx = in ? xsp[m][b] : 127u;
-          acc[m] = mfma_fp4(w[u], sw[u], x, sx, acc[m]);
-        }
+        const u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp + (int64_t)b * 16);
+        const uint32_t sx = xsp[b];
+        acc = mfma_fp4(w[u], in ? sw[u] : 127u, x, in ? sx : 127u, acc);
       } else {
         // the K order of the four products is permuted: lane group g holds block b of its row
         const float s32 = in ? e8m0_or_nan(sw[u]) : 1.0f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const u32x4_t wj = __builtin_bit_cast(u32x4_t, fp4x8_bf16(w[u][j], s32));
-#pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp[m] + (int64_t)b * 64 + 16 * j);
-            if (!in) x = u32x4_t{0, 0, 0, 0};
-            acc[m] = mfma_bf16(wj, x, acc[m]);
-          }
+          u32x4_t x = *reinterpret_cast<const u32x4_t*>(xp + (int64_t)b * 64 + 16 * j);
+          if (!in) x = u32x4_t{0, 0, 0, 0};
+          acc = mfma_bf16(__builtin_bit_cast(u32x4_t, fp4x8_bf16(w[u][j], s32)), x, acc);
         }
       }
     }
   }
-#pragma unroll
-  for (int m = 0; m < MF; ++m) part[kw][f][m][lane] = acc[m];
+  part[kw][f][lane] = acc;
   __syncthreads();
-  // the partial sums of a row fragment: wave m < MF takes row fragment m (and all columns)
-  for (int m = wave; m < MF; m += NT * KW) {
-    const int r = 16 * m + l16;
-    if (16 * m >= t.nrows) break;
-    f32x4_t v[NT];
+  if (wave > 0) return;
+  f32x4_t v[NT];
 #pragma unroll
-    for (int q = 0; q < NT; ++q) {
-      v[q] = part[0][q][m][lane];
+  for (int q = 0; q < NT; ++q) {
+    v[q] = part[0][q][lane];
 #pragma unroll
-      for (int k = 1; k < KW; ++k) v[q] += part[k][q][m][lane];
-    }
-    const int i = t.row0 + min(r, t.nrows - 1);
-    const bool on = r < t.nrows;
-    RowOut o;
-    rows_out<1>(a, &i, &on, &o);
-    with_format(a, [&](auto yf, auto vec) {
-      constexpr int YF = decltype(yf)::value;
-      constexpr bool VEC = decltype(vec)::value;
-      if (a.swiglu) {
-        if (NT == 4) store_pair<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[NT / 2]), swiglu4(v[1], v[NT / 2 + 1 < NT ? NT / 2 + 1 : 0]));
-        else store_one<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[1]));
-      } else {
-#pragma unroll
-        for (int q = 0; q < NT; q += 2) store_pair<YF, VEC>(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
-      }
-    });
+    for (int k = 1; k < KW; ++k) v[q] += part[k][q][lane];
   }
+  const bool on = l16 < t.nrows;
+  RowOut o;
+  rows_out<1>(a, &i_row, &on, &o);
+  with_format(a, [&](auto yf, auto vec) {
+    constexpr int YF = decltype(yf)::value;
+    constexpr bool VEC = decltype(vec)::value;
+    if (a.swiglu) {
+      if constexpr (NT == 4) store_pair<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[2]), swiglu4(v[1], v[3]));
+      else store_one<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[1]));
+    } else {
+#pragma unroll
+      for (int q = 0; q < NT; q += 2) store_pair<YF, VEC>(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
+    }
+  });
 }
 
 // ---------------------------------------------------------------- many rows
@@ -452,12 +428,13 @@ product_few_kernel(ProductArgs a, int n_nb) {
 
 enum { kBf16 = 0, kA16W4 = 1, kFp4 = 2 };
 
-template <int WM_, int WN_, int NF_, int MFX_, int PER_CU_>
+template <int WM_, int WN_, int NF_, int MFX_, int KG_, int PER_CU_>
 struct WideShape {
-  static constexpr int WM = WM_, WN = WN_, NF = NF_, MFX = MFX_;
-  static constexpr int BM = 16 * WM * MFX, BN = 16 * NF * WN, threads = 64 * WM * WN;
+  static constexpr int WM = WM_, WN = WN_, NF = NF_, MFX = MFX_, KG = KG_;
+  static constexpr int BM = 16 * WM * MFX, BN = 16 * NF * WN;
+  static constexpr int group = 64 * WM * WN, threads = group * KG;   // of a K group, of the workgroup
   static constexpr int resident = 256 * PER_CU_;             // workgroups that the chip holds at once
-  static constexpr int waves = PER_CU_ * WM * WN / 4;        // per SIMD
+  static constexpr int waves = PER_CU_ * threads / 256;      // per SIMD
 };
 
 // At most VM loads outstanding, every LDS access done, then the workgroup's barrier.
@@ -517,20 +494,38 @@ struct Scales {
 };
 
 template <int MODE, class S>
-struct WideLds {
+struct WideRing {
   uint8_t x[2][S::BM * 128];
   uint8_t w[2][S::BN * 128];
   // scales of the weight rows, then (MXFP4) of the rows, 16 bytes each
   uint8_t s[MODE == kBf16 ? 1 : 2][MODE == kBf16 ? 16 : (S::BN + (MODE == kFp4 ? S::BM : 0)) * 16];
-  int perm[S::BM];                                // routes of the next tile's rows
+};
+template <int MODE, class S>
+struct WideLds {
+  WideRing<MODE, S> ring[S::KG];
+  int perm[S::KG == 1 ? S::BM : 1];               // routes of the next tile's rows
   int first[kMaxGroups + 1];
+};
+
+// The stages of a row that a K group takes: from `from` on, `n` of them (`most` in the first group,
+// which has the most).
+template <int MODE, class S>
+struct WideShare {
+  int from, n, most;
+  __device__ __forceinline__ WideShare(int stages, int kg) {
+    constexpr int align = MODE == kFp4 ? 2 : MODE == kA16W4 ? 8 : 1;   // scales come for so many at a time
+    const int per = S::KG == 1 ? stages : div_up(div_up(stages, S::KG), align) * align;
+    from = S::KG == 1 ? 0 : kg * per;
+    n = S::KG == 1 ? stages : min(max(stages - from, 0), per);
+    most = S::KG == 1 ? stages : min(stages, per);
+  }
 };
 
 // What a thread loads of a tile: its 16 bytes of every stage, of rows tid / 8 + RQ q, and the scales
 // of one row.
 template <int MODE, class S>
 struct WideSource {
-  static constexpr int T = S::threads, RQ = T / 8, WQ = S::BN / RQ, XQ = S::BM / RQ;
+  static constexpr int T = S::group, RQ = T / 8, WQ = S::BN / RQ, XQ = S::BM / RQ;
   static constexpr int SR = MODE == kBf16 ? 0 : S::BN + (MODE == kFp4 ? S::BM : 0);
   static constexpr int SQ = SR == 0 ? 1 : div_up(SR, T);      // rows of scales per thread: tid + T q
   // offsets (32 bits: launch_wide checks that a matrix and all of x are that small) from the group's
@@ -540,9 +535,11 @@ struct WideSource {
 
   // perm: the routes of the tile's rows (any pointer; unused without a.perm).
   template <class P>
-  __device__ __forceinline__ void point(const ProductArgs& a, const Tile& t, int ch, P perm) {
+  __device__ __forceinline__ void point(const ProductArgs& a, const Tile& t, int ch, int from, P perm) {
     constexpr int HN = S::BN / 2;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % T;
+    // where stage `from` begins: bytes of x and of the weights, scale bytes
+    const int x0 = from * 128, w0 = MODE == kA16W4 ? from * 32 : from * 128, s0 = from * (MODE == kFp4 ? 8 : 2);
     auto x_at = [&](int r) {
       const int m = min(r, t.nrows - 1), i = t.row0 + m;
       return max(x_row(a, i, a.perm ? perm[m] : i), 0);
@@ -555,15 +552,15 @@ struct WideSource {
     };
     wbase = a.w + (int64_t)t.entry * a.N * wrow_b;
 #pragma unroll
-    for (int q = 0; q < WQ; ++q) w[q] = w_row(q * RQ + (tid >> 3)) * wrow_b + ch * 16;
+    for (int q = 0; q < WQ; ++q) w[q] = w_row(q * RQ + (tid >> 3)) * wrow_b + w0 + ch * 16;
 #pragma unroll
-    for (int q = 0; q < XQ; ++q) x[q] = x_at(q * RQ + (tid >> 3)) * xrow_b + ch * 16;
+    for (int q = 0; q < XQ; ++q) x[q] = x_at(q * RQ + (tid >> 3)) * xrow_b + x0 + ch * 16;
     if (MODE != kBf16) {
 #pragma unroll
       for (int q = 0; q < SQ; ++q) {
         const int r = q * T + tid;
-        if (MODE == kFp4 && r >= S::BN) s[q] = a.xs + (int64_t)x_at(r - S::BN) * (K / 32);
-        else s[q] = a.ws + ((int64_t)t.entry * a.N + w_row(min(r, S::BN - 1))) * (K / 32);
+        if (MODE == kFp4 && r >= S::BN) s[q] = a.xs + (int64_t)x_at(r - S::BN) * (K / 32) + s0;
+        else s[q] = a.ws + ((int64_t)t.entry * a.N + w_row(min(r, S::BN - 1))) * (K / 32) + s0;
       }
     }
   }
@@ -575,23 +572,28 @@ struct WideTurn {
 };
 
 template <int MODE, class S, bool SDMA, int MF>
-__device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLds<MODE, S>& lds, const Tile& t,
+__device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLds<MODE, S>& all, const Tile& t,
                                           WideSource<MODE, S>& src, WideTurn& turn, Scales<MODE == kFp4 ? 8 : 2>* sc,
                                           bool more, int b, int total, Tile& next, uint32_t wdst, uint32_t xdst,
                                           uint32_t sdst) {
-  constexpr int WM = S::WM, HN = S::BN / 2, T = S::threads, RQ = T / 8;
+  constexpr int WM = S::WM, HN = S::BN / 2, T = S::group, RQ = T / 8, KG = S::KG;
   constexpr int WQ = S::BN / RQ, XQ = (MF * 16 * WM + RQ - 1) / RQ;
   constexpr int SR = WideSource<MODE, S>::SR, SQ = WideSource<MODE, S>::SQ, NF = S::NF;
   constexpr int period = MODE == kFp4 ? 2 : 8;               // stages that one load of scales covers
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+  const int tid = threadIdx.x % T, lane = tid & 63, wave = tid >> 6, g = lane >> 4, l16 = lane & 15;
+  const int kg = KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  WideRing<MODE, S>& lds = all.ring[kg];
   const int wm = wave % WM, wn = wave / WM;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
   const int c0 = t.nb * (a.swiglu ? HN : S::BN);
-  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;   // bytes of a row in use
-  const int stages = (xb + 127) / 128;
-  const int nblk = a.K / 32;
+  // bytes of a row, and its stages and blocks, from where the K group begins
+  const int row_b = MODE == kFp4 ? a.K / 2 : 2 * a.K;
+  const WideShare<MODE, S> share((row_b + 127) / 128, kg);
+  const int stages = share.n;
+  const int xb = row_b - share.from * 128, wb = MODE == kA16W4 ? a.K / 2 - share.from * 32 : xb;
+  const int nblk = a.K / 32 - share.from * (MODE == kFp4 ? 8 : 2);
   const int ch = (tid & 7) ^ ((tid >> 3) & 7);
-  const uint32_t pdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.perm[0]) + wave * 256);
+  const uint32_t pdst = __builtin_amdgcn_readfirstlane(lds_offset(&all.perm[0]) + wave * 256);
 
   // Scales of period p straight into LDS; or of stage s, in two steps through a register.
   auto request_scales = [&](int p, int at) {
@@ -697,9 +699,9 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
     }
   };
 
-  for (int s = 0; s < stages; ++s) {
+  for (int s = 0; s < share.most; ++s) {
     const bool last = s + 1 == stages;
-    if (MODE == kFp4 && last && (xb & 127)) {
+    if (MODE == kFp4 && last && xb < stages * 128) {
       // chunks past the row's end count as zeros: of one operand, since every e2m1 code is finite
       __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
       asm volatile("" ::: "memory");
@@ -713,7 +715,7 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
     // tile's results, which may still be on their way
     if (s == 0) wait_stage<63>();
     else wait_stage<0>();
-    if (!last) {
+    if (s + 1 < stages) {
       if (MODE != kBf16 && !SDMA) {
 #pragma unroll
         for (int q = 0; q < SQ; ++q) {
@@ -733,14 +735,14 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
     // The workgroup's next tile: looked up while the first stage is computed, its first stage
     // requested while the last one is.  No vector load into registers here: the compiler would
     // wait for it, and so for the stage on its way, before this stage's products.
-    if (s == 0 && more) {
-      next_tile<S::BM>(a, b, total, n_nb, lds.first, &next);
+    if (KG == 1 && s == 0 && more) {
+      next_tile<S::BM>(a, b, total, n_nb, all.first, &next);
       if (a.perm && wave * 64 < S::BM)
         load_lds4(a.perm + next.row0 + min(tid, next.nrows - 1), pdst);
     }
-    if (last && more) {
+    if (KG == 1 && last && more) {
       if (stages == 1) wait_stage<0>();
-      src.point(a, next, ch, lds.perm);
+      src.point(a, next, ch, 0, all.perm);
       const int sn = turn.stage + stages;
       if (MODE != kBf16 && SDMA) request_scales(0, turn.s + (stages + period - 1) / period);
       request_w(0, MODE == kA16W4 ? turn.w + (stages + 3) / 4 : sn);
@@ -748,17 +750,38 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
       for (int q = 0; q < S::BM / RQ; ++q)
         if (q * RQ < next.nrows) request_x(0, sn, q);
     }
-    compute(s, MODE == kFp4 || s * 128 + 64 < xb);
+    if (KG == 1 || s < stages) compute(s, MODE == kFp4 || s * 128 + 64 < xb);
   }
   turn.stage += stages;
   turn.s += (stages + period - 1) / period;
   turn.w += (stages + 3) / 4;
-  if (MODE != kBf16 && !SDMA && more) {
+  if (MODE != kBf16 && !SDMA && KG == 1 && more) {
 #pragma unroll
     for (int q = 0; q < SQ; ++q) {
       put_scales(0, q, Scales<SN>::first(src.s[q], nblk));
       if (stages > 1) sc[q].load(src.s[q], SN, nblk);
     }
+  }
+
+  if constexpr (KG > 1) {
+    // the groups' sums meet in LDS, added in the order of K
+    static_assert(sizeof(all.ring) >= (size_t)(KG - 1) * T * NF * S::MFX * 16, "room for the partial sums");
+    f32x4_t(*part)[NF * MF][T] = reinterpret_cast<f32x4_t(*)[NF * MF][T]>(&all.ring[0]);
+    wait_stage<0>();
+    if (kg > 0) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) part[kg - 1][f * MF + m][tid] = acc[f][m];
+    }
+    wait_stage<0>();
+    if (kg > 0) return;
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+#pragma unroll
+        for (int k = 1; k < KG; ++k) acc[f][m] += part[k - 1][f * MF + m][tid];
   }
 
   int row[MF];
@@ -799,10 +822,9 @@ template <int MODE, class S, bool SDMA>
 __global__ void __launch_bounds__(S::threads, S::waves)
 product_wide_kernel(ProductArgs a, int n_nb) {
   __shared__ __attribute__((aligned(16))) WideLds<MODE, S> lds;
-  const int tid = threadIdx.x, wave = tid >> 6;
   int total;
   if (a.offsets) {
-    if (wave == 0) first_tiles<S::BM>(a, lds.first);
+    if (threadIdx.x < 64) first_tiles<S::BM>(a, lds.first);
     __syncthreads();
     total = __builtin_amdgcn_readfirstlane(lds.first[a.E]) * n_nb;
   } else {
@@ -812,48 +834,57 @@ product_wide_kernel(ProductArgs a, int n_nb) {
   if (b >= total) return;
   Tile t;
   next_tile<S::BM>(a, b, total, n_nb, lds.first, &t);
-  WideSource<MODE, S> src;
-  const int ch = (tid & 7) ^ ((tid >> 3) & 7);
-  src.point(a, t, ch, a.perm + t.row0);
-  const uint32_t wdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.w[0][wave * 1024]));
-  const uint32_t xdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.x[0][wave * 1024]));
-  const uint32_t sdst = __builtin_amdgcn_readfirstlane(lds_offset(&lds.s[0][0]) + wave * 1024);
-  // the first tile's first stage
-  constexpr int T = S::threads, RQ = T / 8, SR = WideSource<MODE, S>::SR, SQ = WideSource<MODE, S>::SQ;
-  const int xb = MODE == kFp4 ? a.K / 2 : 2 * a.K, wb = MODE == kBf16 ? 2 * a.K : a.K / 2;
+  constexpr int T = S::group, RQ = T / 8, SR = WideSource<MODE, S>::SR, SQ = WideSource<MODE, S>::SQ;
   constexpr int SN = MODE == kFp4 ? 8 : 2;
+  const int tid = threadIdx.x % T, wave = tid >> 6;
+  const int kg = S::KG == 1 ? 0 : __builtin_amdgcn_readfirstlane(threadIdx.x / T);
+  WideRing<MODE, S>& ring = lds.ring[kg];
+  const int ch = (tid & 7) ^ ((tid >> 3) & 7);
+  const uint32_t wdst = __builtin_amdgcn_readfirstlane(lds_offset(&ring.w[0][wave * 1024]));
+  const uint32_t xdst = __builtin_amdgcn_readfirstlane(lds_offset(&ring.x[0][wave * 1024]));
+  const uint32_t sdst = __builtin_amdgcn_readfirstlane(lds_offset(&ring.s[0][0]) + wave * 1024);
+  const int row_b = MODE == kFp4 ? a.K / 2 : 2 * a.K;
+  const WideShare<MODE, S> share((row_b + 127) / 128, kg);
+  const int xb = row_b - share.from * 128, wb = MODE == kA16W4 ? a.K / 2 - share.from * 32 : xb;
+  const int nblk = a.K / 32 - share.from * (MODE == kFp4 ? 8 : 2);
+  WideSource<MODE, S> src;
   Scales<SN> sc[SQ] = {};
-  if (MODE != kBf16) {
+  if (S::KG == 1 || share.n > 0) {
+    // the first tile's first stage
+    src.point(a, t, ch, share.from, a.perm + t.row0);
+    if (MODE != kBf16) {
 #pragma unroll
-    for (int q = 0; q < SQ; ++q) {
-      if (SDMA) {
-        if (SR % T == 0 || q * T + wave * 64 < SR) load_lds16(src.s[q], sdst + q * T * 16);
-      } else {
-        const uint64_t v = Scales<SN>::first(src.s[q], a.K / 32);
-        if (SR % T == 0 || q * T + tid < SR) __builtin_memcpy(&lds.s[0][(q * T + tid) * 16], &v, SN);
-        if (xb > 128) sc[q].load(src.s[q], SN, a.K / 32);
+      for (int q = 0; q < SQ; ++q) {
+        if (SDMA) {
+          if (SR % T == 0 || q * T + wave * 64 < SR) load_lds16(src.s[q], sdst + q * T * 16);
+        } else {
+          const uint64_t v = Scales<SN>::first(src.s[q], nblk);
+          if (SR % T == 0 || q * T + tid < SR) __builtin_memcpy(&ring.s[0][(q * T + tid) * 16], &v, SN);
+          if (share.n > 1) sc[q].load(src.s[q], SN, nblk);
+        }
       }
     }
+#pragma unroll
+    for (int q = 0; q < S::BN / RQ; ++q)
+      load_lds16(src.wbase, src.w[q] - (ch * 16 < wb ? 0 : ch * 16), wdst + q * RQ * 128);
+#pragma unroll
+    for (int q = 0; q < S::BM / RQ; ++q)
+      if (q * RQ < t.nrows) load_lds16(a.x, src.x[q] - (ch * 16 < xb ? 0 : ch * 16), xdst + q * RQ * 128);
   }
-#pragma unroll
-  for (int q = 0; q < S::BN / RQ; ++q) load_lds16(src.wbase, src.w[q] - (ch * 16 < wb ? 0 : ch * 16), wdst + q * RQ * 128);
-#pragma unroll
-  for (int q = 0; q < S::BM / RQ; ++q)
-    if (q * RQ < t.nrows) load_lds16(a.x, src.x[q] - (ch * 16 < xb ? 0 : ch * 16), xdst + q * RQ * 128);
   __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
   asm volatile("" ::: "memory");
 
   WideTurn turn{0, 0, 0};
   for (;;) {
     b += gridDim.x;
-    const bool more = b < total;
+    const bool more = S::KG == 1 && b < total;     // with K groups every tile has its own workgroup
     Tile next = t;
     // fragments that the tile's rows need of every wave, the same for the whole workgroup
     const int steps = div_up(t.nrows, 16 * S::WM);
     auto run = [&](auto mf) {
       wide_tile<MODE, S, SDMA, decltype(mf)::value>(a, n_nb, lds, t, src, turn, sc, more, b, total, next, wdst, xdst, sdst);
     };
-    if constexpr (!SDMA) {
+    if constexpr (!SDMA || S::MFX == 2) {
       if (2 * steps <= S::MFX) run(Const<S::MFX / 2>());
       else run(Const<S::MFX>());
     } else if (S::MFX > 4 && steps > 4) {
@@ -915,34 +946,20 @@ static int64_t most_row_tiles(const ProductArgs& a, int64_t bm) {
   return a.offsets ? a.M / bm + (a.E < a.M ? a.E : a.M) : (a.M + bm - 1) / bm;
 }
 
-template <int XF, int WF, int MF, int NT>
-static void launch_few_k(const ProductArgs& a, unsigned grid, int n_nb, int steps, hipStream_t s) {
-  // enough waves along K that a wave has at most 4 steps, up to 16 waves per workgroup
-  if (steps <= 16 || NT == 4)
-    hipLaunchKernelGGL((product_few_kernel<XF, WF, MF, NT, 4>), dim3(grid), dim3(64 * NT * 4), 0, s, a, n_nb);
-  else if constexpr (NT == 2)
-    hipLaunchKernelGGL((product_few_kernel<XF, WF, MF, NT, 8>), dim3(grid), dim3(64 * NT * 8), 0, s, a, n_nb);
-}
-
 template <int XF, int WF>
 static int launch_few(const ProductArgs& a, hipStream_t s) {
   const int nt = a.swiglu && a.y_fmt == MC_MXFP4 ? 4 : 2;
   const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? 8 * nt : 16 * nt;
-  const int64_t n_nb = (n_out + cols - 1) / cols;
-  const int mf = a.M <= 16 ? 1 : a.M <= 32 ? 2 : 4;
-  const int64_t tiles = most_row_tiles(a, 16 * mf) * n_nb;
+  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, 16) * n_nb;
   MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   const int steps = WF == MC_BF16 ? a.K / 32 : (a.K + 127) / 128;
-  const unsigned grid = (unsigned)tiles;
-  if (nt == 4) {
-    if (mf == 1) launch_few_k<XF, WF, 1, 4>(a, grid, (int)n_nb, steps, s);
-    else if (mf == 2) launch_few_k<XF, WF, 2, 4>(a, grid, (int)n_nb, steps, s);
-    else launch_few_k<XF, WF, 4, 4>(a, grid, (int)n_nb, steps, s);
-  } else {
-    if (mf == 1) launch_few_k<XF, WF, 1, 2>(a, grid, (int)n_nb, steps, s);
-    else if (mf == 2) launch_few_k<XF, WF, 2, 2>(a, grid, (int)n_nb, steps, s);
-    else launch_few_k<XF, WF, 4, 2>(a, grid, (int)n_nb, steps, s);
-  }
+  auto run = [&](auto kernel, int kw) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(64 * nt * kw), 0, s, a, (int)n_nb);
+  };
+  // enough waves along K that most have at most kFewSteps steps, up to 16 waves per workgroup
+  if (nt == 4) run(product_few_kernel<XF, WF, 4, 4>, 4);
+  else if (steps <= 4 * kFewSteps) run(product_few_kernel<XF, WF, 2, 4>, 4);
+  else run(product_few_kernel<XF, WF, 2, 8>, 8);
   MC_LAUNCH_CHECK();
   return MC_OK;
 }
@@ -953,7 +970,7 @@ static int launch_wide(const ProductArgs& a, hipStream_t s) {
   const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, S::BM) * n_nb;
   MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   auto run = [&](auto kernel) {
-    const int64_t grid = tiles < S::resident ? tiles : S::resident;
+    const int64_t grid = S::KG > 1 || tiles < S::resident ? tiles : S::resident;
     hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(S::threads), 0, s, a, (int)n_nb);
   };
   const bool sdma = a.K % 512 == 0 && ((uintptr_t)a.xs | (uintptr_t)a.ws) % 16 == 0;
@@ -966,22 +983,41 @@ static int launch_wide(const ProductArgs& a, hipStream_t s) {
   return MC_OK;
 }
 
+// Tiles of a shape, at most.
+template <class S>
+static int64_t most_tiles(const ProductArgs& a) {
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? S::BN / 2 : S::BN;
+  return most_row_tiles(a, S::BM) * ((n_out + cols - 1) / cols);
+}
+
 int launch_product(const ProductArgs& a, hipStream_t s) {
   if (a.M == 0 || a.N == 0 || a.x_rows == 0 || a.y_rows == 0 || a.n == 0) return MC_OK;
-  typedef WideShape<2, 4, 4, 8, 1> Big;           // 256 x 256, one workgroup per CU
-  typedef WideShape<2, 2, 4, 4, 2> Medium;        // 128 x 128, two per CU
-  // bytes of a matrix and of x, which the wide kernels reach with 32-bit offsets
+  typedef WideShape<2, 4, 4, 8, 1, 1> Big;        // 256 x 256, one workgroup per CU
+  typedef WideShape<2, 2, 4, 4, 1, 2> Medium;     // 128 x 128, two per CU
+  typedef WideShape<2, 1, 4, 2, 2, 2> Small2;     // 64 x 64, K in two parts, two per CU
+  typedef WideShape<2, 1, 4, 2, 4, 1> Small4;     // 64 x 64, K in four parts
+  // bytes of a matrix and of x, which the wide kernels reach with 32-bit offsets (beyond, the tiles
+  // of 16 rows read with 64-bit ones)
   const int64_t w_bytes = (int64_t)a.N * (a.w_fmt == MC_BF16 ? 2 * (int64_t)a.K : a.K / 2);
   const int64_t x_bytes = a.x_rows * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
-  if (a.M > 64 && w_bytes <= UINT32_MAX && x_bytes <= UINT32_MAX) {
+  // Up to 16 rows: one token's experts 8 us (12 in Small4), one token 4096 x 2048 6.5 us (9.5); from
+  // 17 rows on Small4 is level or ahead (64 x 4096 x 4096: 19 against 35 us).
+  if (a.M > 16 && w_bytes <= UINT32_MAX && x_bytes <= UINT32_MAX) {
     // The large tiles read each operand half as often, and win where they fill the chip with full
     // tiles: 8192 x 4096 x 4096 in fp4 86 against 101 us, 256 experts of 192 rows 1.40 against
-    // 1.68 ms a layer.  Where groups are small or uneven the small ones win: 24 rows a group 268
-    // against 276 us, 64 groups of 250 rows on average, skewed, 207 against 231 us.
+    // 1.68 ms a layer.  Where groups are small or uneven the 128 x 128 ones win: 24 rows a group
+    // 268 against 276 us, 64 groups of 250 rows on average, skewed, 207 against 231 us.
     const int64_t groups = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
-    const int64_t cols = a.swiglu ? Big::BN / 2 : Big::BN, n_nb = ((a.swiglu ? a.N / 2 : a.N) + cols - 1) / cols;
-    const int64_t tiles = (a.offsets ? a.M / Big::BM + groups / 2 : (a.M + Big::BM - 1) / Big::BM) * n_nb;
-    if (a.M / groups >= 128 && tiles >= (a.offsets ? 1024 : 192)) return launch_wide<Big>(a, s);
+    const int64_t n_nb = most_tiles<Big>(a) / most_row_tiles(a, Big::BM);
+    const int64_t big = (a.offsets ? a.M / Big::BM + groups / 2 : (a.M + Big::BM - 1) / Big::BM) * n_nb;
+    if (a.M / groups >= 128 && big >= (a.offsets ? 1024 : 192)) return launch_wide<Big>(a, s);
+    // Too few tiles for the chip: 64 x 64, with K shared out among the waves, the more the fewer tiles
+    // (bf16 rows x MXFP4: 333 x 4100 x 2080, 390 tiles, 28 us in two parts, 34 in four, 41 in
+    // Medium; 128 x 4096 x 2048, 128 tiles, 16 / 12 / 37 us; 1000 x 4096 x 2080, 1040 tiles, 50 /
+    // 61 / 37 us).
+    const int64_t small = most_tiles<Small4>(a);
+    if (small <= 256) return launch_wide<Small4>(a, s);
+    if (small <= 768) return launch_wide<Small2>(a, s);
     return launch_wide<Medium>(a, s);
   }
   if (a.x_fmt == MC_MXFP4) return launch_few<MC_MXFP4, MC_MXFP4>(a, s);

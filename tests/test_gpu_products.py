@@ -314,6 +314,109 @@ def test_grouped_quantised_results(xf, wf, swiglu, counts, K):
     assert (y[M] == 0xA5).all() and (sc[M] == 0xA5).all()
 
 
+def gpu_operand(g, fmt, *shape, size=1.0):
+    """A random operand made on the GPU, and its float64 values."""
+    if fmt == "bf16":
+        t = (torch.randn(shape, generator=g, device="cuda") * size).to(BF)
+        return t, None, t.double()
+    codes = torch.randint(0, 256, shape[:-1] + (shape[-1] // 2,), dtype=U8, device="cuda", generator=g)
+    e = int(np.log2(size))
+    scales = torch.randint(124 + e, 128 + e, shape[:-1] + (shape[-1] // 32,), dtype=U8, device="cuda", generator=g)
+    nib = torch.stack([codes & 15, codes >> 4], -1).reshape(shape)
+    mag = torch.tensor([0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")[(nib & 7).long()]
+    v = torch.where(nib >= 8, -mag, mag) * torch.exp2(scales.double() - 127).repeat_interleave(32, -1)
+    return codes, scales, v
+
+
+def gpu_check(got, x, w, swiglu, ty, what):
+    """product_bound, swiglu_bound and check, on the GPU."""
+    K = x.shape[1]
+    v = x @ w.t()
+    d = (K + 8) * 2.0 ** -23 * (x.abs() @ w.abs().t()) + 1e-37
+    if swiglu:
+        n = v.shape[1] // 2
+        g, u, dg, du = v[:, :n], v[:, n:], d[:, :n], d[:, n:]
+        s = g * torch.sigmoid(g)
+        v = s * u
+        d = 1.1 * dg * (u.abs() + du) + (s.abs() + 1.1 * dg) * du + v.abs() * (g.abs() + 8) * 2.0 ** -22
+    tol = d + ROUND[ty] * (v.abs() + d)
+    bad = ~((got.double() - v).abs() <= tol)
+    assert not bad.any(), "%s: %d of %d off" % (what, int(bad.sum()), bad.numel())
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("M,N,K", [(8200, 4096, 96), (8200, 4100, 512), (3000, 4096, 1088), (2100, 1000, 288),
+                                   (700, 2048, 1024), (17, 8192, 4096), (250, 333, 8192)])
+def test_large_products(xf, wf, M, N, K):
+    """Sizes where a workgroup takes several tiles, of every tile shape, and where K is shared out among
+    waves; one group, so that all three operand formats run."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + N + K)
+    x, xs, x64 = gpu_operand(g, xf, M, K)
+    w, ws, w64 = gpu_operand(g, wf, 1, N, K, size=2.0 ** -5)
+    y = torch.full((M, N), float("nan"), dtype=F32, device="cuda")
+    mc.grouped_matmul(x, w, torch.tensor([0, M], dtype=I32, device="cuda"), y, x_scale=xs, w_scale=ws)
+    gpu_check(y, x64, w64[0], False, F32, (xf, wf, M, N, K))
+    if wf == "mxfp4":
+        y2 = torch.empty_like(y)
+        mc.mxfp4_matmul(x, w[0], ws[0], y2, x_scale=xs)
+        assert torch.equal(y, y2)
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("E,rows,N,K", [(16, 400, 8192, 96), (64, 24, 4096, 512), (1024, 3, 256, 160), (300, 1, 512, 544),
+                                        (40, 1, 128, 64)])
+def test_many_groups(xf, wf, swiglu, E, rows, N, K):
+    """Many tiles per workgroup over ragged groups (empty ones among them), rows gathered, results
+    scattered with gates."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(E + rows + N + K)
+    r = np.random.default_rng(E + K)
+    counts = r.integers(0, 2 * rows + 1, size=E)
+    counts[r.integers(E)] = 0
+    M = int(counts.sum())
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    x, xs, x64 = gpu_operand(g, xf, M, K)
+    w, ws, w64 = gpu_operand(g, wf, E, N, K, size=2.0 ** -5)
+    perm = r.permutation(M).astype(np.int32)
+    gate = torch.rand(M, device="cuda", generator=g)
+    n_out = N // 2 if swiglu else N
+    y = torch.full((M, n_out), float("nan"), dtype=F32, device="cuda")
+    mc.grouped_matmul(x, w, dev(off), y, x_scale=xs, w_scale=ws, swiglu=swiglu, perm=dev(perm), y_perm=True, gate=gate)
+    p = dev(perm).long()
+    # the gate's product is one more rounding: divide it out in 64 bits and allow for it
+    z = y.double() / gate.double()[:, None]
+    for e in range(E):
+        at = p[off[e]:off[e + 1]]
+        if len(at):
+            gpu_check(z[at], x64[at], w64[e], swiglu, F32, (e, int(counts[e])))
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_rows_beyond_32_bit_offsets(xf, wf):
+    """Rows of x more than 4 GiB behind its start."""
+    K = 2048
+    n = (1 << 32) // (2 * K if xf == "bf16" else K // 2) + 100
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    at = torch.tensor([0, 5, n - 1, n - 2, n - 50] + list(range(n - 40, n - 5)), device="cuda")
+    part, ps, x64 = gpu_operand(g, xf, len(at), K)
+    x = torch.zeros((n, part.shape[1]), dtype=part.dtype, device="cuda")
+    x[at] = part
+    xs = None
+    if ps is not None:
+        xs = torch.zeros((n, K // 32), dtype=U8, device="cuda")
+        xs[at] = ps
+    w, ws, w64 = gpu_operand(g, wf, 2, 160, K, size=2.0 ** -5)
+    M = len(at)
+    y = torch.empty((M, 160), dtype=F32, device="cuda")
+    mc.grouped_matmul(x, w, torch.tensor([0, 7, M], dtype=I32, device="cuda"), y, x_scale=xs, w_scale=ws,
+                      perm=at.to(I32))
+    gpu_check(y[:7], x64[:7], w64[0], False, F32, xf)
+    gpu_check(y[7:], x64[7:], w64[1], False, F32, xf)
+
+
 def test_grouped_entries_and_bad_rows():
     """entry_of leaves groups out or maps them to other matrices; entries, routes and offsets outside
     their ranges skip rows and touch nothing."""
