@@ -11,4 +11,4 @@ from ._lib import (MC_BF16, MC_MXFP4, Banks, Cache, HostPool, McError, abi_versi
                    moe_experts_decode, moe_route, moe_route_lookup, slot_cache_lookup_evict,
                    bandwidth_profile, recommend_backend, cache_install, mxfp4_quantize,
                    mxfp4_dequantize, mxfp4_matmul, grouped_matmul, moe_experts_prefill_act,
-                   prefill_act_ws_bytes)
+                   moe_experts_prefill_act_part, prefill_act_ws_bytes)

@@ -116,6 +116,8 @@ _SIGS = {
     "moe_experts_prefill_act_ws_bytes": (C.c_size_t, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "moe_experts_prefill_act": (C.c_int, [_P, _P, _P, _I32, _I32, _P, _I32, C.POINTER(Banks), _I32, _P,
                                           C.c_size_t, _P, _P, C.POINTER(Prefetch)]),
+    "moe_experts_prefill_act_part": (C.c_int, [_P, _P, _P, _I32, _I32, _P, _I32, C.POINTER(Banks), _P, _I32, _I32,
+                                               _P, C.c_size_t, _P, _P, _P]),
     "mc_host_pool_create": (_P, [_I32, _P]),
     "mc_host_pool_destroy": (None, [_P]),
     "mc_host_pool_cpus": (C.c_int32, [_P, _P, _I32]),
@@ -565,31 +567,54 @@ def prefill_act_ws_bytes(T: int, k: int, E: int, H: int, I: int, act: str) -> in
     return int(lib().moe_experts_prefill_act_ws_bytes(T, k, E, H, I, FMT[act]))
 
 
+def _layer_device(fn: str, x, ids, w, n_tok, H: int, act: str, ws, y, *rest) -> int:
+    """Checks the tensors of a prefill layer call; the GPU they are on."""
+    if act not in FMT:
+        raise ValueError("%s: act must be bf16 or mxfp4, not %r" % (fn, act))
+    if _torch is None:
+        _load_torch()
+    if ids.dim() != 2:
+        raise ValueError("%s: ids has shape %s" % (fn, tuple(ids.shape)))
+    T, k = ids.shape
+    _packed(fn, "ids", ids, (T, k), _torch.int32)
+    _packed(fn, "w", w, (T, k), _torch.float32)
+    for what, t in (("x", x), ("y", y)):
+        if t is None:
+            continue
+        if _etype(t) != MC_BF16:
+            raise ValueError("%s: %s must be bf16, not %s" % (fn, what, t.dtype))
+        _packed(fn, what, t, (T, H), t.dtype)
+    if n_tok is not None:
+        _packed(fn, "n_tok", n_tok, (1,), _torch.int32)
+    return _device(fn, x, ids, w, n_tok, ws, y, *rest)
+
+
 def moe_experts_prefill_act(x, ids, w, n_tok, E: int, layer_buf: Banks, act: str, ws, y,
                             nxt: Optional[Prefetch] = None, stream=None) -> None:
     """Prefill layer on bf16 or MXFP4 activations (act = "bf16" or "mxfp4"): x and y bf16 (values or
     bits) [T][H], ids int32 and w fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes."""
     fn = "moe_experts_prefill_act"
-    if act not in FMT:
-        raise ValueError("%s: act must be bf16 or mxfp4, not %r" % (fn, act))
-    if ids.dim() != 2:
-        raise ValueError("%s: ids has shape %s" % (fn, tuple(ids.shape)))
+    d = _layer_device(fn, x, ids, w, n_tok, layer_buf.H, act, ws, y)
     T, k = ids.shape
-    if _torch is None:
-        _load_torch()
-    _packed(fn, "ids", ids, (T, k), _torch.int32)
-    _packed(fn, "w", w, (T, k), _torch.float32)
-    for what, t in (("x", x), ("y", y)):
-        if _etype(t) != MC_BF16:
-            raise ValueError("%s: %s must be bf16, not %s" % (fn, what, t.dtype))
-        _packed(fn, what, t, (T, layer_buf.H), t.dtype)
-    if n_tok is not None:
-        _packed(fn, "n_tok", n_tok, (1,), _torch.int32)
-    d = _device(fn, x, ids, w, n_tok, ws, y)
     f = lib().moe_experts_prefill_act
     _call(fn, d, stream, lambda st: f(
-        _ptr(x), _ptr(ids), _ptr(w), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], _ptr(ws),
-        ws.numel() * ws.element_size(), _ptr(y), st, C.byref(nxt) if nxt is not None else None))
+        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], ws.data_ptr(),
+        ws.numel() * ws.element_size(), y.data_ptr(), st, C.byref(nxt) if nxt is not None else None))
+
+
+def moe_experts_prefill_act_part(x, ids, w, n_tok, E: int, part_buf: Banks, entry_of, act: str, steps: int, ws,
+                                 counts=None, y=None, stream=None) -> None:
+    """One or more steps of that layer (PF_SORT / PF_EXPERTS / PF_COMBINE) on ws."""
+    fn = "moe_experts_prefill_act_part"
+    d = _layer_device(fn, x, ids, w, n_tok, part_buf.H, act, ws, y, entry_of, counts)
+    T, k = ids.shape
+    for what, t in (("entry_of", entry_of), ("counts", counts)):
+        if t is not None:
+            _packed(fn, what, t, (E,), _torch.int32)
+    f = lib().moe_experts_prefill_act_part
+    _call(fn, d, stream, lambda st: f(
+        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(part_buf), _ptr(entry_of), FMT[act],
+        steps, ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(counts), _ptr(y), st))
 
 
 class HostPool:

@@ -56,77 +56,115 @@ extern "C" size_t moe_experts_prefill_act_ws_bytes(int32_t T, int32_t k, int32_t
   return ws_layout(T, k, E, H, I, act, nullptr, nullptr);
 }
 
-extern "C" int moe_experts_prefill_act(const void* x_bf16, const int32_t* ids, const float* w, int32_t T, int32_t k,
-                                       const int32_t* n_tok, int32_t E, const mc_banks* buf, int32_t act, void* ws,
-                                       size_t ws_bytes, void* y_bf16, hipStream_t s, const mc_prefetch* next) {
-  clear_error();
-  const char* fn = "moe_experts_prefill_act";
+static int check_args(const char* fn, const void* x, const int32_t* ids, const float* w, int32_t T, int32_t k, int32_t E,
+                      const mc_banks* buf, int32_t act, const void* ws, size_t ws_bytes, const void* y, bool need_n,
+                      bool need_y) {
   int rc;
   if ((rc = check_banks(buf, fn)) != MC_OK) return rc;
   MC_REQUIRE(act == MC_BF16 || act == MC_MXFP4, "%s: activations of format %d", fn, act);
   MC_REQUIRE(act == MC_BF16 || buf->fmt == MC_MXFP4, "%s: MXFP4 activations need MXFP4 experts", fn);
   MC_REQUIRE(T >= 0 && k >= 1 && E >= 1 && E <= kP_MaxE && k <= E, "%s: T=%d k=%d E=%d", fn, T, k, E);
   MC_REQUIRE((int64_t)T * k <= 0x7FFFFFFF, "%s: T=%d x k=%d routes are too many", fn, T, k);
-  MC_REQUIRE(buf->n >= E, "%s: layer buffer holds %lld < E=%d experts", fn, (long long)buf->n, E);
-  const int H = buf->H, I = buf->I;
-  MC_REQUIRE(I <= 0x3FFFFFFF, "%s: I=%d is too large", fn, I);
-  const size_t need = moe_experts_prefill_act_ws_bytes(T, k, E, H, I, act);
+  MC_REQUIRE(!need_n || buf->n >= E, "%s: layer buffer holds %lld < E=%d experts", fn, (long long)buf->n, E);
+  MC_REQUIRE(buf->I <= 0x3FFFFFFF, "%s: I=%d is too large", fn, buf->I);
+  const size_t need = moe_experts_prefill_act_ws_bytes(T, k, E, buf->H, buf->I, act);
   MC_REQUIRE(T == 0 || ws_bytes >= need, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
-  MC_REQUIRE(((uintptr_t)x_bf16 | (uintptr_t)ws | (uintptr_t)y_bf16) % 16 == 0, "%s: x, ws and y must be 16-byte aligned",
-             fn);
-  MC_REQUIRE(T == 0 || (x_bf16 && ids && w && ws && y_bf16), "%s: NULL pointer", fn);
-  if (next && (rc = prefetch_launch(fn, next, E)) != MC_OK) return rc;
-  if (T == 0) return MC_OK;
+  MC_REQUIRE(((uintptr_t)x | (uintptr_t)ws | (uintptr_t)y) % 16 == 0, "%s: x, ws and y must be 16-byte aligned", fn);
+  MC_REQUIRE(T == 0 || (x && ids && w && ws && (y || !need_y)), "%s: NULL pointer", fn);
+  return MC_OK;
+}
 
+// The steps of a layer (MC_PF_*) on one workspace.
+static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int32_t T, int32_t k, const int32_t* n_tok,
+                     int32_t E, const mc_banks* buf, const int32_t* entry_of, int32_t act, int32_t steps, void* ws,
+                     int32_t* counts, void* y_bf16, hipStream_t s) {
+  int rc;
+  const int H = buf->H, I = buf->I;
   ActWs v{};
   ws_layout(T, k, E, H, I, act, &v, static_cast<uint8_t*>(ws));
-  if ((rc = sort_routes_launch(ids, T, k, n_tok, E, v.sort, s)) != MC_OK) return rc;
-  if (act == MC_MXFP4 && (rc = mc_mxfp4_quantize(x_bf16, MC_BF16, T, H, H, v.xq, v.xqs, s)) != MC_OK) return rc;
+  if (steps & MC_PF_SORT) {
+    // the counts go straight to the caller's array, if there is one
+    if (counts) v.sort.counts = counts;
+    if ((rc = sort_routes_launch(ids, T, k, n_tok, E, v.sort, s)) != MC_OK) return rc;
+    if (act == MC_MXFP4 && (rc = mc_mxfp4_quantize(x_bf16, MC_BF16, T, H, H, v.xq, v.xqs, s)) != MC_OK) return rc;
+  }
+  if (steps & MC_PF_EXPERTS) {
+    ProductArgs p{};
+    p.E = E;
+    p.n = buf->n;
+    p.M = T * k;
+    p.offsets = v.sort.offsets;
+    p.perm = v.sort.perm;
+    p.entry_of = entry_of;
+    p.x_fmt = act;
+    p.w_fmt = buf->fmt;
+    // h = silu(x W_gate^T) * (x W_up^T), rows in sorted order
+    p.x = act == MC_MXFP4 ? v.xq : static_cast<const uint8_t*>(x_bf16);
+    p.xs = v.xqs;
+    p.ldx = H;
+    p.x_rows = T;
+    p.x_div = k;
+    p.x_perm = 1;
+    p.w = static_cast<const uint8_t*>(buf->gate_up);
+    p.ws = static_cast<const uint8_t*>(buf->gate_up_scale);
+    p.N = 2 * I;
+    p.K = H;
+    p.swiglu = 1;
+    p.y = v.h;
+    p.ys = v.hs;
+    p.y_fmt = act;
+    p.ldy = I;
+    p.y_rows = T * k;
+    if ((rc = launch_product(p, s)) != MC_OK) return rc;
+    // the gated route outputs
+    p.x = v.h;
+    p.xs = v.hs;
+    p.ldx = I;
+    p.x_rows = T * k;
+    p.x_perm = 0;
+    p.w = static_cast<const uint8_t*>(buf->down);
+    p.ws = static_cast<const uint8_t*>(buf->down_scale);
+    p.N = H;
+    p.K = I;
+    p.swiglu = 0;
+    p.y = reinterpret_cast<uint8_t*>(v.yr);
+    p.ys = nullptr;
+    p.y_fmt = MC_F32;
+    p.ldy = H;
+    p.y_perm = 1;
+    p.gate = w;
+    p.n_gate = T * k;
+    if ((rc = launch_product(p, s)) != MC_OK) return rc;
+  }
+  if (steps & MC_PF_COMBINE)
+    return combine_launch(ids, T, k, E, H, n_tok, v.yr, static_cast<uint16_t*>(y_bf16), s);
+  return MC_OK;
+}
 
-  ProductArgs p{};
-  p.E = E;
-  p.n = buf->n;
-  p.M = T * k;
-  p.offsets = v.sort.offsets;
-  p.perm = v.sort.perm;
-  p.x_fmt = act;
-  p.w_fmt = buf->fmt;
-  // h = silu(x W_gate^T) * (x W_up^T), rows in sorted order
-  p.x = act == MC_MXFP4 ? v.xq : static_cast<const uint8_t*>(x_bf16);
-  p.xs = v.xqs;
-  p.ldx = H;
-  p.x_rows = T;
-  p.x_div = k;
-  p.x_perm = 1;
-  p.w = static_cast<const uint8_t*>(buf->gate_up);
-  p.ws = static_cast<const uint8_t*>(buf->gate_up_scale);
-  p.N = 2 * I;
-  p.K = H;
-  p.swiglu = 1;
-  p.y = v.h;
-  p.ys = v.hs;
-  p.y_fmt = act;
-  p.ldy = I;
-  p.y_rows = T * k;
-  if ((rc = launch_product(p, s)) != MC_OK) return rc;
-  // the gated route outputs
-  p.x = v.h;
-  p.xs = v.hs;
-  p.ldx = I;
-  p.x_rows = T * k;
-  p.w = static_cast<const uint8_t*>(buf->down);
-  p.ws = static_cast<const uint8_t*>(buf->down_scale);
-  p.N = H;
-  p.K = I;
-  p.swiglu = 0;
-  p.x_perm = 0;
-  p.y = reinterpret_cast<uint8_t*>(v.yr);
-  p.ys = nullptr;
-  p.y_fmt = MC_F32;
-  p.ldy = H;
-  p.y_perm = 1;
-  p.gate = w;
-  p.n_gate = T * k;
-  if ((rc = launch_product(p, s)) != MC_OK) return rc;
-  return combine_launch(ids, T, k, E, H, n_tok, v.yr, static_cast<uint16_t*>(y_bf16), s);
+extern "C" int moe_experts_prefill_act(const void* x_bf16, const int32_t* ids, const float* w, int32_t T, int32_t k,
+                                       const int32_t* n_tok, int32_t E, const mc_banks* buf, int32_t act, void* ws,
+                                       size_t ws_bytes, void* y_bf16, hipStream_t s, const mc_prefetch* next) {
+  clear_error();
+  const char* fn = "moe_experts_prefill_act";
+  int rc;
+  if ((rc = check_args(fn, x_bf16, ids, w, T, k, E, buf, act, ws, ws_bytes, y_bf16, true, true)) != MC_OK) return rc;
+  if (next && (rc = prefetch_launch(fn, next, E)) != MC_OK) return rc;
+  if (T == 0) return MC_OK;
+  return act_steps(x_bf16, ids, w, T, k, n_tok, E, buf, nullptr, act, MC_PF_ALL, ws, nullptr, y_bf16, s);
+}
+
+extern "C" int moe_experts_prefill_act_part(const void* x_bf16, const int32_t* ids, const float* w, int32_t T, int32_t k,
+                                            const int32_t* n_tok, int32_t E, const mc_banks* part_buf,
+                                            const int32_t* entry_of, int32_t act, int32_t steps, void* ws,
+                                            size_t ws_bytes, int32_t* counts, void* y_bf16, hipStream_t s) {
+  clear_error();
+  const char* fn = "moe_experts_prefill_act_part";
+  int rc;
+  MC_REQUIRE(steps != 0 && (steps & ~MC_PF_ALL) == 0, "%s: steps=0x%x", fn, steps);
+  if ((rc = check_args(fn, x_bf16, ids, w, T, k, E, part_buf, act, ws, ws_bytes, y_bf16, false,
+                       (steps & MC_PF_COMBINE) != 0)) != MC_OK)
+    return rc;
+  MC_REQUIRE(!(steps & MC_PF_EXPERTS) || entry_of, "%s: the experts step needs entry_of", fn);
+  if (T == 0) return MC_OK;
+  return act_steps(x_bf16, ids, w, T, k, n_tok, E, part_buf, entry_of, act, steps, ws, counts, y_bf16, s);
 }

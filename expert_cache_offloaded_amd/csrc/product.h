@@ -6,6 +6,8 @@
 
 namespace mc {
 
+constexpr int kMaxGroups = 1024;
+
 struct ProductArgs {
   const uint8_t* x;           // rows of x: bf16, or MXFP4 codes
   const uint8_t* xs;          // their scales (MXFP4)
@@ -29,6 +31,10 @@ struct ProductArgs {
 
 // Enqueues the product; the arguments have been checked (check_product).
 int launch_product(const ProductArgs& a, hipStream_t s);
+// ... of bf16 x bf16, bf16 x MXFP4 and MXFP4 x MXFP4, something to do
+int launch_product_bf16(const ProductArgs& a, hipStream_t s);
+int launch_product_a16w4(const ProductArgs& a, hipStream_t s);
+int launch_product_fp4(const ProductArgs& a, hipStream_t s);
 int check_product(const char* fn, const ProductArgs& a);
 
 }  // namespace mc

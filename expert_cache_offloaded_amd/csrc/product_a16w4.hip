@@ -1,0 +1,8 @@
+// Products of bf16 rows x MXFP4 matrices.
+#include "product_dev.h"
+
+namespace mc {
+
+int launch_product_a16w4(const ProductArgs& a, hipStream_t s) { return launch_by_size<MC_BF16, MC_MXFP4>(a, s); }
+
+}  // namespace mc

@@ -57,6 +57,31 @@ class BankSet:
         return BankSet({k: v[i:i + 1] for k, v in self.t.items()}, self.H, self.I, self.fmt)
 
 
+def quantize_banks(src: BankSet, dst: BankSet, device="cuda") -> None:
+    """bf16 experts -> MXFP4 experts (``mxfp4_quantize`` on every row of every bank), e.g. a bf16
+    checkpoint's host pool -> the host pool that fills the slots.  Both sets hold the same n, H
+    and I, each in host or device memory; entries pass through the GPU a few at a time.  The
+    results are complete when the call returns."""
+    if src.fmt != "bf16" or dst.fmt != "mxfp4":
+        raise ValueError("quantize_banks turns bf16 banks into MXFP4 ones, not %s into %s" % (src.fmt, dst.fmt))
+    if (src.n, src.H, src.I) != (dst.n, dst.H, dst.I):
+        raise ValueError("quantize_banks: %s against %s entries, H, I"
+                         % ((src.n, src.H, src.I), (dst.n, dst.H, dst.I)))
+    for name in ("gate_up", "down"):
+        s, codes, scales = src.t[name], dst.t[name], dst.t[name + "_scale"]
+        step = max(1, (64 << 20) // (s[0].numel() * 2))
+        for i in range(0, src.n, step):
+            j = min(i + step, src.n)
+            rows, cols = (j - i) * s.shape[1], s.shape[2]
+            v = s[i:j].to(device).view(rows, cols)
+            c = torch.empty((rows, cols // 2), dtype=torch.uint8, device=v.device)
+            e = torch.empty((rows, cols // 32), dtype=torch.uint8, device=v.device)
+            L.mxfp4_quantize(v, c, e)
+            codes[i:j].copy_(c.view(codes[i:j].shape))
+            scales[i:j].copy_(e.view(scales[i:j].shape))
+    torch.cuda.synchronize(device)
+
+
 class CacheState:
     """Device tables of the cross-layer LRU (caller-owned memory)."""
 
@@ -268,13 +293,23 @@ class PrefillRunner:
         gives the route counts, read back to the host), the experts of each group, one
         combine — and its output is bit-identical to the whole-layer call.
     After the last layer the experts left in the buffers are installed in the cache
-    (mc_cache_install on the freshly reset tables)."""
+    (mc_cache_install on the freshly reset tables).
 
-    def __init__(self, cache: "CacheState", host: "BankSet", pool: "BankSet", T: int, k: int):
+    act chooses the activations of the layers: "mxfp4" (MXFP4 experts; x and h quantised,
+    moe_experts_prefill_act) or "bf16" (either format, h rounded to bf16); by default MXFP4
+    experts run on bf16 activations with h in fp16 (moe_experts_prefill), bf16 experts on
+    "bf16"."""
+
+    def __init__(self, cache: "CacheState", host: "BankSet", pool: "BankSet", T: int, k: int,
+                 act: Optional[str] = None):
         E = cache.E
         if pool.n < 1:
             raise ValueError("prefill needs at least one slot")
-        self.cache, self.host, self.pool, self.T, self.k = cache, host, pool, T, k
+        if act is None and pool.fmt == "bf16":
+            act = "bf16"
+        if act not in (None, "bf16", "mxfp4") or (act == "mxfp4" and pool.fmt != "mxfp4"):
+            raise ValueError("act must be bf16, mxfp4 (with MXFP4 experts) or None, not %r" % (act,))
+        self.cache, self.host, self.pool, self.T, self.k, self.act = cache, host, pool, T, k, act
         self.double = pool.n >= 2 * E
         dev = pool.t["gate_up"].device
         if self.double:
@@ -283,7 +318,9 @@ class PrefillRunner:
             self.G, nb = max(1, pool.n // 2), (2 if pool.n >= 2 else 1)
         self.bufs = [BankSet({n: v[b * self.G:(b + 1) * self.G] for n, v in pool.t.items()}, pool.H, pool.I,
                              pool.fmt) for b in range(nb)]
-        self.ws = torch.empty(L.prefill_ws_bytes(T, k, E, pool.H, pool.I), dtype=torch.uint8, device=dev)
+        ws_bytes = (L.prefill_ws_bytes(T, k, E, pool.H, pool.I) if act is None else
+                    L.prefill_act_ws_bytes(T, k, E, pool.H, pool.I, act))
+        self.ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
         self.ids = torch.empty((T, k), dtype=torch.int32, device=dev)
         self.w = torch.empty((T, k), dtype=torch.float32, device=dev)
         if not self.double:
@@ -312,6 +349,24 @@ class PrefillRunner:
                     v[j:r + 1].copy_(self.host.t[n][f0:f0 + r - j + 1], non_blocking=True)
                 j = r + 1
 
+    def _layer(self, x, b: int, y, nxt, stream) -> None:
+        """The whole layer whose experts buffer b holds."""
+        E, desc = self.cache.E, self.bufs[b].desc
+        if self.act is None:
+            L.moe_experts_prefill(x, self.ids, self.w, None, E, desc, self.ws, y, nxt, stream)
+        else:
+            L.moe_experts_prefill_act(x, self.ids, self.w, None, E, desc, self.act, self.ws, y, nxt, stream)
+
+    def _part(self, x, b: int, entry_of, steps: int, stream, counts=None, y=None) -> None:
+        """Steps of a layer with the experts in buffer b."""
+        E, desc = self.cache.E, self.bufs[b].desc
+        if self.act is None:
+            L.moe_experts_prefill_part(x, self.ids, self.w, None, E, desc, entry_of, steps, self.ws, counts=counts,
+                                       y=y, stream=stream)
+        else:
+            L.moe_experts_prefill_act_part(x, self.ids, self.w, None, E, desc, entry_of, self.act, steps, self.ws,
+                                           counts=counts, y=y, stream=stream)
+
     def run(self, logits, x, ys, renorm: int = 1):
         """logits: list of L device fp32 [T, E]; x: device bf16 bits [T, H]; ys: list of L
         device bf16 [T, H] outputs.  Resets the cache first; returns the installed ids
@@ -336,8 +391,7 @@ class PrefillRunner:
                     copy.wait_event(free[1 - b])
                     nxt = L.make_prefetch(self.host.desc, (layer + 1) * E, self.bufs[1 - b].desc, copy)
                 L.moe_route(logits[layer], self.k, renorm, self.ids, self.w, comp)
-                L.moe_experts_prefill(x, self.ids, self.w, None, E, self.bufs[b].desc, self.ws, ys[layer], nxt,
-                                      comp)
+                self._layer(x, b, ys[layer], nxt, comp)
                 if nxt is not None:
                     done[1 - b].record(copy)
                 free[b].record(comp)
@@ -347,8 +401,7 @@ class PrefillRunner:
             G = self.G
             for layer in range(Lc):
                 L.moe_route(logits[layer], self.k, renorm, self.ids, self.w, comp)
-                L.moe_experts_prefill_part(x, self.ids, self.w, None, E, self.bufs[0].desc, None, L.PF_SORT,
-                                           self.ws, counts=self.counts, stream=comp)
+                self._part(x, 0, None, L.PF_SORT, comp, counts=self.counts)
                 routed = np.nonzero(self.counts.cpu().numpy())[0]      # waits for the sort
                 groups = [routed[i:i + G] for i in range(0, len(routed), G)]
                 self.groups.append(groups)
@@ -365,12 +418,10 @@ class PrefillRunner:
                     self._copy_group(layer, grp, b, copy)
                     done[b].record(copy)
                     comp.wait_event(done[b])
-                    L.moe_experts_prefill_part(x, self.ids, self.w, None, E, self.bufs[b].desc, self.entry_of[g],
-                                               L.PF_EXPERTS, self.ws, stream=comp)
+                    self._part(x, b, self.entry_of[g], L.PF_EXPERTS, comp)
                     free[b].record(comp)
                     held[b] = [layer * E + int(e) for e in grp]
-                L.moe_experts_prefill_part(x, self.ids, self.w, None, E, self.bufs[0].desc, None, L.PF_COMBINE,
-                                           self.ws, y=ys[layer], stream=comp)
+                self._part(x, 0, None, L.PF_COMBINE, comp, y=ys[layer])
         # the experts left in the buffers become the decode cache
         flats = []
         for b in range(nb):

@@ -550,6 +550,17 @@ int moe_experts_prefill_act(const void* x_bf16, const int32_t* ids, const float*
                             int32_t act, void* ws, size_t ws_bytes, void* y_bf16, hipStream_t s,
                             const mc_prefetch* next);
 
+/*
+ * The same layer in steps (MC_PF_SORT, which also quantises x; MC_PF_EXPERTS for the experts of
+ * part_buf by entry_of; MC_PF_COMBINE), as moe_experts_prefill_part; the result of a layer's
+ * steps is bit-identical to moe_experts_prefill_act's.
+ */
+int moe_experts_prefill_act_part(const void* x_bf16, const int32_t* ids, const float* w, int32_t T,
+                                 int32_t k, const int32_t* n_tok, int32_t E,
+                                 const mc_banks* part_buf, const int32_t* entry_of, int32_t act,
+                                 int32_t steps, void* ws, size_t ws_bytes, int32_t* counts,
+                                 void* y_bf16, hipStream_t s);
+
 /* ------------------------------------------------------------------------- */
 /* Hybrid split / merge and the host branch                                  */
 /* ------------------------------------------------------------------------- */

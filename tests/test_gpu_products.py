@@ -629,3 +629,100 @@ def test_layer_near_the_bf16_activation_layer():
     mc._lib.moe_experts_prefill(x.cuda(), dev(ids), dev(w), None, E, mc.make_banks("mxfp4", H, I, banks), ws, y0)
     # three independent roundings to bf16 (h, y, y0), each at most 2^-8 / sqrt 3 rms
     assert float((y - y0.double()).norm() / y0.double().norm()) <= 3 ** 0.5 * 2.0 ** -8 / 3 ** 0.5
+
+
+# ---------------------------------------------------------------- in the framework's own paths
+
+@pytest.mark.parametrize("where", ["cpu", "cuda"])
+def test_quantize_banks(where):
+    """bf16 experts to MXFP4 experts, from and to host or device memory: the oracle's codes and
+    scales, and a layer that runs on them."""
+    from expert_cache_offloaded_amd.runtime import BankSet, alloc_banks, quantize_banks
+    n, H, I = 3, 128, 64
+    src, dst = (alloc_banks(n, H, I, f, device=where, pin=where == "cpu") for f in ("bf16", "mxfp4"))
+    r = np.random.default_rng(2)
+    for v in src.values():
+        v.copy_(torch.from_numpy(r.standard_normal(tuple(v.shape)) * 0.02).to(BF).view(torch.int16))
+    a, b = BankSet(src, H, I, "bf16"), BankSet(dst, H, I, "mxfp4")
+    quantize_banks(a, b)
+    for name in ("gate_up", "down"):
+        c, s = encode_mxfp4(bf16_to_f64(src[name].cpu().numpy().view(np.uint16)))
+        assert np.array_equal(dst[name].cpu().numpy(), c)
+        assert np.array_equal(dst[name + "_scale"].cpu().numpy(), s)
+    with pytest.raises(ValueError):
+        quantize_banks(b, a)
+    with pytest.raises(ValueError):
+        quantize_banks(a, BankSet(alloc_banks(n + 1, H, I, "mxfp4", device=where), H, I, "mxfp4"))
+
+
+@pytest.mark.parametrize("fmt,act", [("bf16", None), ("bf16", "bf16"), ("mxfp4", "mxfp4"), ("mxfp4", "bf16")])
+@pytest.mark.parametrize("S", [32, 9, 1])
+def test_prefill_runner_on_chosen_activations(fmt, act, S):
+    """PrefillRunner with bf16 experts and with quantised activations: two whole layers in the pool,
+    a pool that loads the routed experts in groups, and a single slot all give moe_experts_prefill_act's
+    outputs bit for bit, and leave the last layer's experts in the cache."""
+    from expert_cache_offloaded_amd.runtime import BankSet, CacheState, PrefillRunner, alloc_banks
+    Lc, E, T, k, H, I = 2, 12, 70, 3, 128, 192
+    r = np.random.default_rng(S)
+    host = alloc_banks(Lc * E, H, I, fmt, pin=True)
+    for name, v in host.items():
+        if name.endswith("scale"):
+            v.copy_(torch.from_numpy(r.integers(118, 122, tuple(v.shape)).astype(np.uint8)))
+        elif fmt == "mxfp4":
+            v.copy_(torch.from_numpy(r.integers(0, 256, tuple(v.shape)).astype(np.uint8)))
+        else:
+            v.copy_(torch.from_numpy(r.standard_normal(tuple(v.shape)) * 0.02).to(BF).view(torch.int16))
+    pool = BankSet(alloc_banks(S, H, I, fmt, device="cuda"), H, I, fmt)
+    cache = CacheState(Lc, E, S)
+    logits = [dev(r.standard_normal((T, E)).astype(np.float32)) for _ in range(Lc)]
+    x = dev(r.standard_normal((T, H)).astype(np.float32)).to(BF).view(torch.int16)
+    ys = [torch.empty((T, H), dtype=torch.int16, device="cuda") for _ in range(Lc)]
+    run = PrefillRunner(cache, BankSet(host, H, I, fmt), pool, T, k, act=act)
+    held = run.run(logits, x, ys)
+    torch.cuda.synchronize()
+    assert cache.t["id_of"].cpu().tolist()[:len(held)] == held
+    a = act or "bf16"
+    for layer in range(Lc):
+        ids, w = torch.empty((T, k), dtype=I32, device="cuda"), torch.empty((T, k), device="cuda")
+        mc.moe_route(logits[layer], k, 1, ids, w)
+        banks = {n: v[layer * E:(layer + 1) * E].cuda() for n, v in host.items()}
+        ws = torch.empty(mc.prefill_act_ws_bytes(T, k, E, H, I, a), dtype=U8, device="cuda")
+        y = torch.empty_like(ys[layer])
+        mc.moe_experts_prefill_act(x, ids, w, None, E, mc.make_banks(fmt, H, I, banks), a, ws, y)
+        assert torch.equal(ys[layer], y), layer
+    if fmt == "bf16":
+        with pytest.raises(ValueError):
+            PrefillRunner(cache, BankSet(host, H, I, fmt), pool, T, k, act="mxfp4")
+
+
+def test_layer_graph_replay_with_changing_batches():
+    """A captured quantised layer replayed with other tokens, routes and valid counts, eager layers and
+    synchronisations in between: each replay equals the eager call."""
+    T, k, E, H, I = 96, 2, 16, 128, 128
+    rng = np.random.default_rng(12)
+    gu, gus, _ = operand(rng, "mxfp4", E, 2 * I, H, size=2.0 ** -4)
+    dn, dns, _ = operand(rng, "mxfp4", E, H, I, size=2.0 ** -4)
+    banks = {"gate_up": gu, "gate_up_scale": gus, "down": dn, "down_scale": dns}
+    desc = mc.make_banks("mxfp4", H, I, banks)
+    x, y = (torch.zeros((T, H), dtype=BF, device="cuda") for _ in range(2))
+    y2 = torch.empty_like(y)
+    ids, w = torch.zeros((T, k), dtype=I32, device="cuda"), torch.zeros((T, k), device="cuda")
+    nt = torch.tensor([T], dtype=I32, device="cuda")
+    ws, ws2 = (torch.empty(mc.prefill_act_ws_bytes(T, k, E, H, I, "mxfp4"), dtype=U8, device="cuda") for _ in range(2))
+    mc.moe_experts_prefill_act(x, ids, w, nt, E, desc, "mxfp4", ws, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        mc.moe_experts_prefill_act(x, ids, w, nt, E, desc, "mxfp4", ws, y)
+    for seed, n in enumerate((T, 17, 0, 50)):
+        r = np.random.default_rng(seed)
+        x.copy_(torch.from_numpy(r.standard_normal((T, H))).to(BF))
+        ids.copy_(torch.from_numpy(np.stack([r.permutation(E)[:k] for _ in range(T)]).astype(np.int32)))
+        w.copy_(torch.from_numpy(r.random((T, k)).astype(np.float32)))
+        nt.fill_(n)
+        y.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        mc.moe_experts_prefill_act(x, ids, w, nt, E, desc, "mxfp4", ws2, y2)
+        assert torch.equal(y, y2)
+        assert (y[n:] == 0).all() and (n == 0 or bool((y[:n] != 0).any()))

@@ -143,6 +143,9 @@ def test_prefill_act_refusals():
                dict(ws=None), dict(y=None), dict(x=p + 8), dict(ws=p + 8), dict(ws_bytes=1000),
                dict(nxt=C.byref(empty_next))):
         assert call(**kw) == L.MC_EINVAL, kw
+    part = lambda steps, entry, y=p: lib.moe_experts_prefill_act_part(  # noqa: E731
+        p, p, p, 2, 2, None, 4, C.byref(b), entry, 1, steps, p, big, None, y, None)
+    assert part(0, p) == part(8, p) == part(L.PF_EXPERTS, None) == part(L.PF_COMBINE, p, None) == L.MC_EINVAL
     n = lib.moe_experts_prefill_act_ws_bytes
     assert n(2, 2, 4, 64, 64, 2) == 0 and n(-1, 2, 4, 64, 64, 1) == 0
     assert n(100, 2, 4, 64, 64, 1) < n(100, 2, 4, 64, 64, 0)
