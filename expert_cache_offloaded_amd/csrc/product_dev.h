@@ -86,6 +86,21 @@ __device__ __forceinline__ void place_ungrouped(const ProductArgs& a, int p, int
   t->nrows = min(bm, a.M - t->row0);
 }
 
+// Row tiles of groups base + 64 c + lane, c < 4: all tables are read before the first is used.
+template <int BM>
+__device__ __forceinline__ void group_tiles(const ProductArgs& a, int base, int* m) {
+  const int lane = threadIdx.x & 63;
+  int rows[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const int e = base + 64 * c + lane;
+    int lo;
+    rows[c] = group_rows(a, a.offsets, a.entry_of, min(e, a.E - 1), &lo);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) m[c] = base + 64 * c + lane < a.E ? div_up(rows[c], BM) : 0;
+}
+
 // Tile b of the call, group by group.  Every wave runs the search by itself: lane l looks at group
 // 64 c + l, a prefix sum over the lanes gives each group's first tile.
 template <int BM>
@@ -95,22 +110,23 @@ __device__ __forceinline__ bool find_tile(const ProductArgs& a, int b, int n_nb,
     place_ungrouped(a, b, BM, n_nb, t);
     return true;
   }
-  const int lane = threadIdx.x & 63;
   const int j = b / n_nb;
   int before = 0;
-  for (int base = 0; base < a.E; base += 64) {
-    const int e = base + lane;
-    int lo;
-    const int m = e < a.E ? div_up(group_rows(a, a.offsets, a.entry_of, e, &lo), BM) : 0;
-    const int incl = lane_prefix(m);
-    const uint64_t past = __ballot(before + incl > j);
-    if (past) {
-      const int src = __ffsll((unsigned long long)past) - 1;
-      const int first = before + __builtin_amdgcn_readlane(incl - m, src);
-      place_in_group(a, base + src, b - first * n_nb, BM, n_nb, t);
-      return true;
+  for (int base = 0; base < a.E; base += 256) {
+    int m[4];
+    group_tiles<BM>(a, base, m);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int incl = lane_prefix(m[c]);
+      const uint64_t past = __ballot(before + incl > j);
+      if (past) {
+        const int src = __ffsll((unsigned long long)past) - 1;
+        const int first = before + __builtin_amdgcn_readlane(incl - m[c], src);
+        place_in_group(a, base + 64 * c + src, b - first * n_nb, BM, n_nb, t);
+        return true;
+      }
+      before += __builtin_amdgcn_readlane(incl, 63);
     }
-    before += __builtin_amdgcn_readlane(incl, 63);
   }
   return false;
 }
@@ -121,13 +137,15 @@ template <int BM>
 __device__ __forceinline__ void first_tiles(const ProductArgs& a, int* first) {
   const int lane = threadIdx.x & 63;
   int before = 0;
-  for (int base = 0; base < a.E; base += 64) {
-    const int e = base + lane;
-    int lo;
-    const int m = e < a.E ? div_up(group_rows(a, a.offsets, a.entry_of, e, &lo), BM) : 0;
-    const int incl = lane_prefix(m);
-    if (e < a.E) first[e] = before + incl - m;
-    before += __builtin_amdgcn_readlane(incl, 63);
+  for (int base = 0; base < a.E; base += 256) {
+    int m[4];
+    group_tiles<BM>(a, base, m);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int e = base + 64 * c + lane, incl = lane_prefix(m[c]);
+      if (e < a.E) first[e] = before + incl - m[c];
+      before += __builtin_amdgcn_readlane(incl, 63);
+    }
   }
   if (lane == 0) first[a.E] = before;
 }
@@ -237,8 +255,12 @@ __device__ __forceinline__ void store_pair(const ProductArgs& a, const RowOut& o
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v0[i]), __float_as_uint(v1[i]), false, false);
-    v[i] = o.gate * __uint_as_float(s[0]);        // 1 without gates
-    v[4 + i] = o.gate * __uint_as_float(s[1]);
+    v[i] = __uint_as_float(s[0]);
+    v[4 + i] = __uint_as_float(s[1]);
+  }
+  if (a.gate) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= o.gate;
   }
   const int col = col0 + 16 * (g & 1) + 8 * (g >> 1);
   if (YF == MC_MXFP4) {
@@ -285,9 +307,12 @@ __device__ __forceinline__ void with_format(const ProductArgs& a, F f) {
 }
 
 __device__ __forceinline__ f32x4_t swiglu4(const f32x4_t& g, const f32x4_t& u) {
+  // g u / (1 + e^-g) with the exponential's and the reciprocal's instructions (each off by a unit or
+  // so in 2^23): an exact division took four times the instructions of all the rest
   f32x4_t h;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i];
+  for (int i = 0; i < 4; ++i)
+    h[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g[i] * -1.442695040888963f)) * u[i];
   return h;
 }
 
@@ -509,11 +534,12 @@ struct WideLds {
 
 // The stages of a row that a K group takes: from `from` on, `n` of them (`most` in the first group,
 // which has the most).
-template <int MODE, class S>
+template <int MODE, class S, bool SDMA>
 struct WideShare {
   int from, n, most;
   __device__ __forceinline__ WideShare(int stages, int kg) {
-    constexpr int align = MODE == kFp4 ? 2 : MODE == kA16W4 ? 8 : 1;   // scales come for so many at a time
+    // scales (SDMA) and kA16W4's weights come in for so many stages at a time
+    constexpr int align = MODE == kFp4 && SDMA ? 2 : MODE != kA16W4 ? 1 : SDMA ? 8 : 4;
     const int per = S::KG == 1 ? stages : div_up(div_up(stages, S::KG), align) * align;
     from = S::KG == 1 ? 0 : kg * per;
     n = S::KG == 1 ? stages : min(max(stages - from, 0), per);
@@ -588,7 +614,7 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
   const int c0 = t.nb * (a.swiglu ? HN : S::BN);
   // bytes of a row, and its stages and blocks, from where the K group begins
   const int row_b = MODE == kFp4 ? a.K / 2 : 2 * a.K;
-  const WideShare<MODE, S> share((row_b + 127) / 128, kg);
+  const WideShare<MODE, S, SDMA> share((row_b + 127) / 128, kg);
   const int stages = share.n;
   const int xb = row_b - share.from * 128, wb = MODE == kA16W4 ? a.K / 2 - share.from * 32 : xb;
   const int nblk = a.K / 32 - share.from * (MODE == kFp4 ? 8 : 2);
@@ -844,7 +870,7 @@ product_wide_kernel(ProductArgs a, int n_nb) {
   const uint32_t xdst = __builtin_amdgcn_readfirstlane(lds_offset(&ring.x[0][wave * 1024]));
   const uint32_t sdst = __builtin_amdgcn_readfirstlane(lds_offset(&ring.s[0][0]) + wave * 1024);
   const int row_b = MODE == kFp4 ? a.K / 2 : 2 * a.K;
-  const WideShare<MODE, S> share((row_b + 127) / 128, kg);
+  const WideShare<MODE, S, SDMA> share((row_b + 127) / 128, kg);
   const int xb = row_b - share.from * 128, wb = MODE == kA16W4 ? a.K / 2 - share.from * 32 : xb;
   const int nblk = a.K / 32 - share.from * (MODE == kFp4 ? 8 : 2);
   WideSource<MODE, S> src;
