@@ -356,8 +356,9 @@ product_few_kernel(ProductArgs a, int n_nb) {
   const int64_t wrow_b = WF == MC_BF16 ? 2 * K : K / 2, xrow_b = XF == MC_BF16 ? 2 * a.ldx : K / 2;
   const int nblk = a.K / 32;
   const int steps = WF == MC_BF16 ? nblk : (nblk + 3) / 4;
-  const int wrow = a.swiglu ? min(c0 + (f % (NT / 2)) * 16 + l16, n_out - 1) + (f >= NT / 2 ? n_out : 0)
-                            : min(c0 + f * 16 + l16, n_out - 1);
+  constexpr int HT = NT > 1 ? NT / 2 : 1;
+  const int wrow = NT > 1 && a.swiglu ? min(c0 + (f % HT) * 16 + l16, n_out - 1) + (f >= HT ? n_out : 0)
+                                      : min(c0 + f * 16 + l16, n_out - 1);
   const uint8_t* wp = a.w + ((int64_t)t.entry * a.N + wrow) * wrow_b;
   const uint8_t* wsp = a.ws + ((int64_t)t.entry * a.N + wrow) * (K / 32);
   const int i_row = t.row0 + min(l16, t.nrows - 1);
@@ -425,7 +426,9 @@ product_few_kernel(ProductArgs a, int n_nb) {
     constexpr bool VEC = decltype(vec)::value;
     if (a.swiglu) {
       if constexpr (NT == 4) store_pair<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[2]), swiglu4(v[1], v[3]));
-      else store_one<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[1]));
+      else if constexpr (NT == 2) store_one<YF, VEC>(a, o, c0, n_out, swiglu4(v[0], v[1]));
+    } else if constexpr (NT == 1) {
+      store_one<YF, VEC>(a, o, c0, n_out, v[0]);
     } else {
 #pragma unroll
       for (int q = 0; q < NT; q += 2) store_pair<YF, VEC>(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
@@ -938,9 +941,12 @@ inline int64_t most_row_tiles(const ProductArgs& a, int64_t bm) {
 
 template <int XF, int WF>
 int launch_few(const ProductArgs& a, hipStream_t s) {
-  const int nt = a.swiglu && a.y_fmt == MC_MXFP4 ? 4 : 2;
-  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, cols = a.swiglu ? 8 * nt : 16 * nt;
-  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = most_row_tiles(a, 16) * n_nb;
+  const int64_t n_out = a.swiglu ? a.N / 2 : a.N, rt = most_row_tiles(a, 16);
+  // as narrow as the epilogue allows (a block of quantised results is 32 columns) where 32 columns
+  // would not fill the chip (8 x 4096 x 4096: 7 against 11 us)
+  const int nt = a.swiglu ? (a.y_fmt == MC_MXFP4 ? 4 : 2) : a.y_fmt != MC_MXFP4 && rt * ((n_out + 31) / 32) <= 256 ? 1 : 2;
+  const int64_t cols = a.swiglu ? 8 * nt : 16 * nt;
+  const int64_t n_nb = (n_out + cols - 1) / cols, tiles = rt * n_nb;
   MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   const int steps = WF == MC_BF16 ? a.K / 32 : (a.K + 127) / 128;
   auto run = [&](auto kernel, int kw) {
@@ -948,6 +954,7 @@ int launch_few(const ProductArgs& a, hipStream_t s) {
   };
   // enough waves along K that most have at most kFewSteps steps, up to 16 waves per workgroup
   if (nt == 4) run(product_few_kernel<XF, WF, 4, 4>, 4);
+  else if (nt == 1) run(product_few_kernel<XF, WF, 1, 8>, 8);
   else if (steps <= 4 * kFewSteps) run(product_few_kernel<XF, WF, 2, 4>, 4);
   else run(product_few_kernel<XF, WF, 2, 8>, 8);
   MC_LAUNCH_CHECK();
@@ -987,14 +994,16 @@ int launch_by_size(const ProductArgs& a, hipStream_t s) {
   constexpr int MODE = WF == MC_BF16 ? kBf16 : XF == MC_BF16 ? kA16W4 : kFp4;
   typedef WideShape<2, 4, 4, 8, 1, 1> Big;        // 256 x 256, one workgroup per CU
   typedef WideShape<2, 2, 4, 4, 1, 2> Medium;     // 128 x 128, two per CU
+  typedef WideShape<2, 2, 4, 4, 2, 1> Medium2;    // 128 x 128, K in two parts
   typedef WideShape<2, 1, 4, 2, 2, 2> Small2;     // 64 x 64, K in two parts, two per CU
   typedef WideShape<2, 1, 4, 2, 4, 1> Small4;     // 64 x 64, K in four parts
   // bytes of a matrix and of x, which the wide kernels reach with 32-bit offsets (beyond, the tiles
   // of 16 rows read with 64-bit ones)
   const int64_t w_bytes = (int64_t)a.N * (a.w_fmt == MC_BF16 ? 2 * (int64_t)a.K : a.K / 2);
   const int64_t x_bytes = a.x_rows * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
-  // Up to 16 rows: one token's experts 8 us (12 in Small4), one token 4096 x 2048 6.5 us (9.5); from
-  // 17 rows on Small4 is level or ahead (64 x 4096 x 4096: 19 against 35 us).
+  // Up to 16 rows: one token's experts 8 us (12 in Small4), 8 x 4096 x 4096 7 us (16); from 17 rows on
+  // Small4 is level or ahead (17 x 4096 x 2048 bf16: 8 against 12 us, 64 x 4096 x 4096: 19 against
+  // 35 us).
   if (a.M > 16 && w_bytes <= UINT32_MAX && x_bytes <= UINT32_MAX) {
     // The large tiles read each operand half as often, and win where they fill the chip with full
     // tiles: 8192 x 4096 x 4096 in fp4 86 against 101 us, 256 experts of 192 rows 1.40 against
@@ -1004,13 +1013,13 @@ int launch_by_size(const ProductArgs& a, hipStream_t s) {
     const int64_t n_nb = most_tiles<Big>(a) / most_row_tiles(a, Big::BM);
     const int64_t big = (a.offsets ? a.M / Big::BM + groups / 2 : (a.M + Big::BM - 1) / Big::BM) * n_nb;
     if (a.M / groups >= 128 && big >= (a.offsets ? 1024 : 192)) return launch_wide<MODE, Big>(a, s);
-    // Too few tiles for the chip: 64 x 64, with K shared out among the waves, the more the fewer tiles
-    // (bf16 rows x MXFP4: 333 x 4100 x 2080, 390 tiles, 28 us in two parts, 34 in four, 41 in
-    // Medium; 128 x 4096 x 2048, 128 tiles, 16 / 12 / 37 us; 1000 x 4096 x 2080, 1040 tiles, 50 /
-    // 61 / 37 us).
+    // Too few tiles for the chip: smaller ones, or K shared out among the waves (bf16 rows x MXFP4, us
+    // in Small4 / Small2 / Medium: 128 x 4096 x 2048, 128 tiles of 64 x 64, 12 / 16 / 37; 333 x 4100 x
+    // 2080, 390 tiles, 34 / 25 / 41; 1000 x 4096 x 2080, 1024 tiles, 61 / 50 / 37 and in Medium2 30).
     const int64_t small = most_tiles<Small4>(a);
     if (small <= 256) return launch_wide<MODE, Small4>(a, s);
     if (small <= 768) return launch_wide<MODE, Small2>(a, s);
+    if (most_tiles<Medium2>(a) <= 256) return launch_wide<MODE, Medium2>(a, s);
     return launch_wide<MODE, Medium>(a, s);
   }
   return launch_few<XF, WF>(a, s);
