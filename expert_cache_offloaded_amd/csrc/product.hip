@@ -11,6 +11,8 @@ int check_product(const char* fn, const ProductArgs& a) {
   MC_REQUIRE(a.y_fmt == MC_BF16 || a.y_fmt == MC_F32 || a.y_fmt == MC_MXFP4, "%s: unknown y format %d", fn, a.y_fmt);
   MC_REQUIRE(a.M >= 0 && a.N >= 0 && a.K >= 32 && a.K % 32 == 0, "%s: M=%d N=%d K=%d (K must be a positive multiple of 32)",
              fn, a.M, a.N, a.K);
+  // tile and byte counts stay within 32 bits
+  MC_REQUIRE(a.M <= 0x7FFF0000 && a.N <= 0x7FFF0000 && a.K <= 1 << 28, "%s: M=%d N=%d K=%d too large", fn, a.M, a.N, a.K);
   MC_REQUIRE(a.E >= 1 && a.E <= kMaxGroups, "%s: E=%d must be in [1, %d]", fn, a.E, kMaxGroups);
   MC_REQUIRE(a.swiglu == 0 || a.swiglu == 1, "%s: swiglu=%d", fn, a.swiglu);
   MC_REQUIRE(!a.swiglu || a.N % 2 == 0, "%s: N=%d must be even with swiglu", fn, a.N);

@@ -298,7 +298,8 @@ struct Const {
 };
 template <class F>
 __device__ __forceinline__ void with_format(const ProductArgs& a, F f) {
-  const bool vec = (a.ldy & 7) == 0;
+  // 16-byte stores, from a column divisible by 8
+  const bool vec = (a.ldy & (a.y_fmt == MC_F32 ? 3 : 7)) == 0;
   if (a.y_fmt == MC_MXFP4) f(Const<MC_MXFP4>(), Const<1>());
   else if (a.y_fmt == MC_F32 && vec) f(Const<MC_F32>(), Const<1>());
   else if (a.y_fmt == MC_F32) f(Const<MC_F32>(), Const<0>());

@@ -474,8 +474,8 @@ int mc_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int
  *   w, w_scale  device MXFP4 [N][K/2], [N][K/32]
  *   y    device, y_fmt MC_BF16 or MC_F32, [M] rows ldy elements apart (ldy >= N)
  * x, w and y are 16-byte aligned, scales have any alignment.  Products are exact and summed
- * in fp32 (the order depends on the sizes only), each result is rounded once.  K % 32 == 0,
- * K >= 32; M = 0 or N = 0 enqueues nothing.  A NaN scale makes the results that read it NaN.
+ * in fp32 (the order depends on sizes and alignment only), each result is rounded once.  K % 32 == 0,
+ * 32 <= K <= 2^28; M and N up to 2^31 - 2^16; M = 0 or N = 0 enqueues nothing.  A NaN scale makes the results that read it NaN.
  * y may not overlap an input.
  */
 int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt, int64_t ldx, const void* w,
@@ -505,8 +505,8 @@ int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt, int64_t l
  * [offsets[0], offsets[E]), and rows of groups whose entry is outside [0, n) (-1: not in this
  * part).  A row with negative r, whose row of x, row of y or gate is outside [0, x_rows),
  * [0, y_rows) or [0, n_gate), is skipped.  With y_perm the entries of perm in use have to differ.
- * K % 32 == 0, K >= 32, 1 <= E <= 1024, N even with swiglu.  Fixed summation order (by the
- * sizes only): results are run-to-run identical.  No workspace, no host synchronisation;
+ * K % 32 == 0, 32 <= K <= 2^28, 1 <= E <= 1024, N even with swiglu.  Fixed summation order (by
+ * sizes and alignment only): results are run-to-run identical.  No workspace, no host synchronisation;
  * capturable, and the group sizes may change between replays.
  */
 typedef struct {
@@ -531,12 +531,13 @@ int mc_grouped_matmul(const mc_grouped* g, hipStream_t s);
 /*
  * Prefill MoE layer with a choice of activations, for bf16 experts too (moe_experts_prefill
  * is MXFP4 experts on bf16 activations):
- *   y[t] = bf16_rne( sum_j w[t][j] * W_down q(silu(W_gate q(x[t])) * (W_up q(x[t]))) )
+ *   y[t] = bf16_rne( sum_j r(w[t][j] * W_down q(silu(W_gate q(x[t])) * (W_up q(x[t])))) )
  * for t < *n_tok (else 0) over the valid routes, q rounding to the activations' format:
  *   act MC_MXFP4  MXFP4 experts; x and h are quantised (mc_mxfp4_quantize's rule) and the
  *                 products run on the matrix cores' fp4 instructions, four times the bf16
- *                 rate; the quantisation costs about 0.1-0.15 relative to bf16 activations
- *   act MC_BF16   MXFP4 or bf16 experts; x is bf16 already, h is rounded to bf16
+ *                 rate; the quantisation costs about 0.1-0.15 relative to bf16 activations.
+ *                 r rounds a route's output to bf16
+ *   act MC_BF16   MXFP4 or bf16 experts; x is bf16 already, h is rounded to bf16; r is nothing
  * Sort, gate_up product with SwiGLU (and the quantisation of h) in its epilogue, down product
  * with the gates, and a fixed-order sum of each token's routes: results are run-to-run
  * identical.  Sums are fp32.  Any T >= 0, E <= 1024, k <= E; H and I multiples of 64.

@@ -558,10 +558,11 @@ def run_layer(x, ids, w, n_tok, E, H, I, fmt, act, banks):
 def test_layer(act, fmt, T, k, E, H, I, n_tok):
     """Against the layer's formula in 64 bits.  bf16: h is rounded to bf16, 2^-8 of itself at most, so
     with A_d = sum_n |W_down[d][n] h[n]| the outputs are off by 2^-8 A_d and their own rounding, and by
-    the fp32 sums, which are far smaller.  MXFP4: the same inputs are quantised on both sides; a value
-    of h that lies within the fp32 sums' error of a rounding border may take the neighbouring code,
-    which moves an output by one code's share; such values are rare, so the outputs are held to the
-    rms bound the bf16 rounding of y sets (2^-8 / sqrt 3, a uniform rounding error, plus a tenth)."""
+    the fp32 sums, which are far smaller.  MXFP4: the same inputs are quantised on both sides, and the
+    routes' outputs rounded to bf16; a value of h that lies within the fp32 sums' error of a rounding
+    border may take the neighbouring code, which moves an output by one code's share; such values are
+    rare, so the outputs are held to the rms bound the bf16 rounding of y sets (2^-8 / sqrt 3, a
+    uniform rounding error, plus a tenth)."""
     rng = np.random.default_rng(T + H + I)
     ids, w, x, banks, gu, dn = layer_inputs(rng, T, k, E, H, I, fmt)
     ids[rng.random(ids.shape) < 0.03] = -1
@@ -583,7 +584,8 @@ def test_layer(act, fmt, T, k, E, H, I, n_tok):
                 h = decode_mxfp4(*encode_mxfp4(h[None]))[0]
             else:
                 mag[t] += w[t, j] * (np.abs(dn[e]) @ np.abs(h))
-            ref[t] += w[t, j] * (dn[e] @ h)
+            r = w[t, j] * (dn[e] @ h)
+            ref[t] += torch.from_numpy(r).to(BF).double().numpy() if act == "mxfp4" else r
     if act == "bf16":
         tol = (2.0 ** -8 + (H + I) * 2.0 ** -22) * mag + 2.0 ** -8 * np.abs(ref) * 1.01
         assert (np.abs(y - ref) <= tol).all()
@@ -605,7 +607,7 @@ def test_layer_is_its_parts():
     xq, xqs = torch.empty((T, H // 2), dtype=U8, device="cuda"), torch.empty((T, H // 32), dtype=U8, device="cuda")
     hq = torch.empty((T * k, I // 2), dtype=U8, device="cuda")
     hqs = torch.empty((T * k, I // 32), dtype=U8, device="cuda")
-    yr = torch.empty((T * k, H), dtype=F32, device="cuda")
+    yr = torch.empty((T * k, H), dtype=BF, device="cuda")
     mc.mxfp4_quantize(x, xq, xqs)
     mc.grouped_matmul(xq, banks["gate_up"], off, hq, x_scale=xqs, w_scale=banks["gate_up_scale"], y_scale=hqs,
                       swiglu=True, perm=perm, x_div=k)

@@ -86,6 +86,8 @@ def test_matmul_refusals():
 
     for kw in (dict(xf=2), dict(xf=3), dict(yf=1), dict(yf=3), dict(M=-1), dict(N=-1), dict(K=0), dict(K=48),
                dict(xf=0, ldx=32), dict(xf=0, ldx=68), dict(ldy=3), dict(x=None), dict(w=None), dict(y=None),
+               dict(K=(1 << 28) + 32, ldx=1 << 29), dict(M=(1 << 31) - 1),
+               dict(N=(1 << 31) - 1, ldy=1 << 31),
                dict(ws=None), dict(xs=None), dict(x=p + 8), dict(w=p + 1), dict(y=p + 2), dict(ldy=1 << 31)):
         assert call(**kw) == L.MC_EINVAL, kw
         assert "mc_mxfp4_matmul" in L.last_error()
