@@ -338,13 +338,11 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t w, uint32_t sw, u32x4_t x, u
 // rows), NT x KW waves: a wave multiplies one 16-row weight fragment over every KW-th
 // step of K (64 bytes of each weight row per step), operands straight from memory, and the KW
 // partial sums meet in LDS in a fixed order.  With few rows the weights are read once and bound
-// the product; what counts is that all of a wave's loads are on their way at once (kFewSteps steps
-// per round) and that even a small matrix fills the chip, hence the split of K over waves
+// the product; what counts is that all of a wave's loads are on their way at once (STEPS steps per
+// round) and that even a small matrix fills the chip, hence the split of K over waves
 // and the narrow tiles.
 
-constexpr int kFewSteps = 4;
-
-template <int XF, int WF, int NT, int KW>
+template <int XF, int WF, int NT, int KW, int STEPS>
 __global__ void __launch_bounds__(64 * NT * KW)
 product_few_kernel(ProductArgs a, int n_nb) {
   __shared__ f32x4_t part[KW][NT][64];
@@ -369,12 +367,12 @@ product_few_kernel(ProductArgs a, int n_nb) {
   const uint8_t* xsp = a.xs + xr * (K / 32);
 
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int s0 = kw; s0 < steps; s0 += KW * kFewSteps) {
-    u32x4_t w[kFewSteps];
-    uint32_t sw[kFewSteps];
+  for (int s0 = kw; s0 < steps; s0 += KW * STEPS) {
+    u32x4_t w[STEPS];
+    uint32_t sw[STEPS];
     // steps and blocks past the end re-read the last ones and count as zeros
 #pragma unroll
-    for (int u = 0; u < kFewSteps; ++u) {
+    for (int u = 0; u < STEPS; ++u) {
       const int s = min(s0 + u * KW, steps - 1);
       if (WF == MC_BF16) {
         w[u] = *reinterpret_cast<const u32x4_t*>(wp + (int64_t)s * 64 + 16 * g);
@@ -385,7 +383,7 @@ product_few_kernel(ProductArgs a, int n_nb) {
       }
     }
 #pragma unroll
-    for (int u = 0; u < kFewSteps; ++u) {
+    for (int u = 0; u < STEPS; ++u) {
       const int s = min(s0 + u * KW, steps - 1);
       const bool in = s0 + u * KW < steps && (WF == MC_BF16 || 4 * s + g < nblk);
       const int b = WF == MC_BF16 ? s : min(4 * s + g, nblk - 1);
@@ -964,11 +962,16 @@ int launch_few(const ProductArgs& a, hipStream_t s) {
   auto run = [&](auto kernel, int kw) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(64 * nt * kw), 0, s, a, (int)n_nb);
   };
-  // enough waves along K that most have at most kFewSteps steps, up to 16 waves per workgroup
-  if (nt == 4) run(product_few_kernel<XF, WF, 4, 4>, 4);
-  else if (nt == 1) run(product_few_kernel<XF, WF, 1, 8>, 8);
-  else if (steps <= 4 * kFewSteps) run(product_few_kernel<XF, WF, 2, 4>, 4);
-  else run(product_few_kernel<XF, WF, 2, 8>, 8);
+  // Waves along K x steps in flight per wave: loads of steps past the end cost what others do, so both
+  // follow K (one token 4096 x 2048 4.5 us in 8 x 2, 5.8 in 8 x 4, 4.6 in 16 x 1; 8 x 8192 x 2048 7.1 /
+  // 11.8 / 8.3; one token's eight experts 1024 x 2048 7.3 in 4 x 4, 7.6 in 8 x 2; 2048 x 512 8.8 / 8.3
+  // and 6.6 in 4 x 2).
+  if (nt == 4) run(product_few_kernel<XF, WF, 4, 4, 4>, 4);
+  else if (nt == 1 && steps <= 16) run(product_few_kernel<XF, WF, 1, 8, 2>, 8);
+  else if (nt == 1) run(product_few_kernel<XF, WF, 1, 8, 4>, 8);
+  else if (steps <= 8) run(product_few_kernel<XF, WF, 2, 4, 2>, 4);
+  else if (steps <= 16) run(product_few_kernel<XF, WF, 2, 4, 4>, 4);
+  else run(product_few_kernel<XF, WF, 2, 8, 4>, 8);
   MC_LAUNCH_CHECK();
   return MC_OK;
 }
