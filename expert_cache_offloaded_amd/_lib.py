@@ -463,6 +463,8 @@ def mxfp4_quantize(src, codes, scales, stream=None) -> None:
     [rows][cols/2] and scales u8 [rows][cols/32]."""
     fn = "mxfp4_quantize"
     cols = _codes(fn, "codes", codes, scales)
+    if codes.dim() != 2:
+        raise ValueError("%s: codes must be 2-D, not of shape %s" % (fn, tuple(codes.shape)))
     rows = codes.shape[0]
     ld = _rows(fn, "src", src, cols, rows)
     _call("mc_mxfp4_quantize", _device(fn, src, codes, scales), stream, lib().mc_mxfp4_quantize, src.data_ptr(),
@@ -473,6 +475,8 @@ def mxfp4_dequantize(codes, scales, dst, stream=None) -> None:
     """The values of MXFP4 rows, to dst (bf16, fp16 or fp32 [rows][cols]; rows may lie apart)."""
     fn = "mxfp4_dequantize"
     cols = _codes(fn, "codes", codes, scales)
+    if codes.dim() != 2:
+        raise ValueError("%s: codes must be 2-D, not of shape %s" % (fn, tuple(codes.shape)))
     rows = codes.shape[0]
     ld = _rows(fn, "dst", dst, cols, rows)
     _call("mc_mxfp4_dequantize", _device(fn, dst, codes, scales), stream, lib().mc_mxfp4_dequantize, codes.data_ptr(),

@@ -184,3 +184,15 @@ def test_binding_refusals():
         d.update(kw)
         with pytest.raises(ValueError):
             mc.grouped_matmul(d.pop("x"), d.pop("w"), d.pop("offsets"), d.pop("y"), **d)
+
+
+@pytest.mark.parametrize("lead", [(), (2, 1)])
+def test_binding_wants_codes_in_rows(lead):
+    """Codes of one or three dimensions, whose first one is not their number of rows, are refused for
+    their shape: as [16] codes of one row they would be taken for 16 rows."""
+    import expert_cache_offloaded_amd as mc
+    codes, scales = torch.zeros(*lead, 16, dtype=torch.uint8), torch.zeros(*lead, 1, dtype=torch.uint8)
+    wide = torch.zeros(codes.shape[0], 32, dtype=torch.bfloat16)
+    for call in (lambda: mc.mxfp4_quantize(wide, codes, scales), lambda: mc.mxfp4_dequantize(codes, scales, wide)):
+        with pytest.raises(ValueError, match="2-D"):
+            call()
