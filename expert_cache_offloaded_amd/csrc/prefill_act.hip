@@ -110,9 +110,10 @@ static int check_args(const char* fn, const void* x, const int32_t* ids, const f
   MC_REQUIRE(act == MC_BF16 || act == MC_MXFP4, "%s: activations of format %d", fn, act);
   MC_REQUIRE(act == MC_BF16 || buf->fmt == MC_MXFP4, "%s: MXFP4 activations need MXFP4 experts", fn);
   MC_REQUIRE(T >= 0 && k >= 1 && E >= 1 && E <= kP_MaxE && k <= E, "%s: T=%d k=%d E=%d", fn, T, k, E);
-  MC_REQUIRE((int64_t)T * k <= 0x7FFFFFFF, "%s: T=%d x k=%d routes are too many", fn, T, k);
+  // the products' limits (check_product)
+  MC_REQUIRE((int64_t)T * k <= 0x7FFF0000, "%s: T=%d x k=%d routes are too many", fn, T, k);
+  MC_REQUIRE(buf->H <= 1 << 28 && buf->I <= 1 << 28, "%s: H=%d I=%d too large", fn, buf->H, buf->I);
   MC_REQUIRE(!need_n || buf->n >= E, "%s: layer buffer holds %lld < E=%d experts", fn, (long long)buf->n, E);
-  MC_REQUIRE(buf->I <= 0x3FFFFFFF, "%s: I=%d is too large", fn, buf->I);
   const size_t need = moe_experts_prefill_act_ws_bytes(T, k, E, buf->H, buf->I, act);
   MC_REQUIRE(T == 0 || ws_bytes >= need, "%s: workspace %zu < %zu bytes", fn, ws_bytes, need);
   MC_REQUIRE(((uintptr_t)x | (uintptr_t)ws | (uintptr_t)y) % 16 == 0, "%s: x, ws and y must be 16-byte aligned", fn);

@@ -114,5 +114,9 @@ extern "C" int mc_grouped_matmul(const mc_grouped* g, hipStream_t s) {
   int rc;
   if ((rc = check_product("mc_grouped_matmul", a)) != MC_OK) return rc;
   MC_REQUIRE(a.offsets || a.M == 0, "mc_grouped_matmul: offsets is NULL");
+  // the kernels' sums over groups stay within 32 bits whatever offsets holds: descending ones let groups
+  // overlap, each with up to M rows
+  MC_REQUIRE((((int64_t)a.M + 15) / 16) * a.E <= 0x7FFFFFFF, "mc_grouped_matmul: M=%d rows of E=%d groups are too many", a.M,
+             a.E);
   return launch_product(a, s);
 }

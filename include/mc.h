@@ -505,7 +505,7 @@ int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt, int64_t l
  * [offsets[0], offsets[E]), and rows of groups whose entry is outside [0, n) (-1: not in this
  * part).  A row with negative r, whose row of x, row of y or gate is outside [0, x_rows),
  * [0, y_rows) or [0, n_gate), is skipped.  With y_perm the entries of perm in use have to differ.
- * K % 32 == 0, 32 <= K <= 2^28, 1 <= E <= 1024, N even with swiglu.  Fixed summation order (by
+ * K % 32 == 0, 32 <= K <= 2^28, 1 <= E <= 1024, E M / 16 < 2^31, N even with swiglu.  Fixed summation order (by
  * sizes and alignment only): results are run-to-run identical.  No workspace, no host synchronisation;
  * capturable, and the group sizes may change between replays.
  */
@@ -540,7 +540,8 @@ int mc_grouped_matmul(const mc_grouped* g, hipStream_t s);
  *   act MC_BF16   MXFP4 or bf16 experts; x is bf16 already, h is rounded to bf16; r is nothing
  * Sort, gate_up product with SwiGLU (and the quantisation of h) in its epilogue, down product
  * with the gates, and a fixed-order sum of each token's routes: results are run-to-run
- * identical.  Sums are fp32.  Any T >= 0, E <= 1024, k <= E; H and I multiples of 64.
+ * identical.  Sums are fp32.  T >= 0, T k <= 2^31 - 2^16, E <= 1024, k <= E; H and I multiples of
+ * 64, up to 2^28.
  *   ws  device workspace of moe_experts_prefill_act_ws_bytes bytes, 16-byte aligned, one per
  *       call in flight; next: as in moe_experts_prefill (layer_buf's format and shape).
  */

@@ -196,3 +196,21 @@ def test_binding_wants_codes_in_rows(lead):
     for call in (lambda: mc.mxfp4_quantize(wide, codes, scales), lambda: mc.mxfp4_dequantize(codes, scales, wide)):
         with pytest.raises(ValueError, match="2-D"):
             call()
+
+
+def test_sizes_past_32_bit_sums_are_refused():
+    """Sizes whose tile sums or row offsets would leave 32 bits (of the grouped product even where
+    groups overlap) are refused for that, before anything is enqueued."""
+    from expert_cache_offloaded_amd import _lib as L
+    lib = L.lib()
+    keep, p = _buf()
+    d = dict(x_fmt=0, w_fmt=1, y_fmt=0, E=1024, M=(1 << 25) + 1, N=64, K=64, x_rows=2, x_div=1, y_rows=2, ldx=64, ldy=64,
+             n=2, x=p, x_scale=p, w=p, w_scale=p, y=p, offsets=p)
+    assert lib.mc_grouped_matmul(C.byref(L.Grouped(**d)), None) == L.MC_EINVAL
+    assert "too many" in L.last_error()
+    b = L.Banks()
+    for T, H, I, word in (((1 << 31) - 1, 64, 64, "too many"), (2, 1 << 29, 64, "too large"), (2, 64, 1 << 29, "too large")):
+        b.fmt, b.H, b.I, b.n = L.MC_MXFP4, H, I, 4
+        b.gate_up = b.gate_up_scale = b.down = b.down_scale = p
+        assert lib.moe_experts_prefill_act(p, p, p, T, 1, None, 4, C.byref(b), 1, p, 1 << 62, p, None, None) == L.MC_EINVAL
+        assert word in L.last_error(), (T, H, I)
