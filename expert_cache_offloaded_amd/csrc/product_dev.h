@@ -340,14 +340,10 @@ __device__ __forceinline__ f32x4_t mfma_fp4(u32x4_t w, uint32_t sw, u32x4_t x, u
 // partial sums meet in LDS in a fixed order.  With few rows the weights are read once and bound
 // the product; what counts is that all of a wave's loads are on their way at once (STEPS steps per
 // round) and that even a small matrix fills the chip, hence the split of K over waves
-// and the narrow tiles.
+// and the narrow tiles.  A launch holds less than 2^32 threads; beyond, workgroups take several tiles.
 
 template <int XF, int WF, int NT, int KW, int STEPS>
-__global__ void __launch_bounds__(64 * NT * KW)
-product_few_kernel(ProductArgs a, int n_nb) {
-  __shared__ f32x4_t part[KW][NT][64];
-  Tile t;
-  if (!find_tile<16>(a, blockIdx.x, n_nb, &t)) return;
+__device__ __forceinline__ void few_tile(const ProductArgs& a, const Tile& t, f32x4_t (*part)[NT][64]) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, g = lane >> 4, l16 = lane & 15;
   const int f = wave % NT, kw = wave / NT;
   const int n_out = a.swiglu ? a.N / 2 : a.N;
@@ -434,6 +430,20 @@ product_few_kernel(ProductArgs a, int n_nb) {
       for (int q = 0; q < NT; q += 2) store_pair<YF, VEC>(a, o, c0 + 16 * q, n_out, v[q], v[q + 1]);
     }
   });
+}
+
+template <int XF, int WF, int NT, int KW, int STEPS>
+__global__ void __launch_bounds__(64 * NT * KW)
+product_few_kernel(ProductArgs a, int n_nb, uint32_t tiles) {
+  __shared__ f32x4_t part[KW][NT][64];
+  for (uint32_t b = blockIdx.x;;) {
+    Tile t;
+    if (!find_tile<16>(a, b, n_nb, &t)) return;
+    few_tile<XF, WF, NT, KW, STEPS>(a, t, part);
+    b += gridDim.x;
+    if (b >= tiles) return;
+    __syncthreads();                               // the sums have been read
+  }
 }
 
 // ---------------------------------------------------------------- many rows
@@ -567,21 +577,24 @@ struct WideSource {
   static constexpr int T = S::group, RQ = T / 8, WQ = S::BN / RQ, XQ = S::BM / RQ;
   static constexpr int SR = MODE == kBf16 ? 0 : S::BN + (MODE == kFp4 ? S::BM : 0);
   static constexpr int SQ = SR == 0 ? 1 : div_up(SR, T);      // rows of scales per thread: tid + T q
-  // offsets (32 bits: launch_wide checks that a matrix and all of x are that small) from the group's
-  // matrix and from x; the scales' address
-  const uint8_t *wbase, *s[SQ];
+  // offsets (32 bits: launch_by_size checks that a matrix and x are that small) from the group's
+  // matrix and from x, or, where a tile's rows lie one behind the other, from the first of them; the
+  // scales' address
+  const uint8_t *wbase, *xbase, *s[SQ];
   uint32_t w[WQ], x[XQ];
 
-  // perm: the routes of the tile's rows (any pointer; unused without a.perm).
+  // perm: the routes of the tile's rows (any pointer; unused without a.x_perm).
   template <class P>
   __device__ __forceinline__ void point(const ProductArgs& a, const Tile& t, int ch, int from, P perm) {
     constexpr int HN = S::BN / 2;
     const int tid = threadIdx.x % T;
     // where stage `from` begins: bytes of x and of the weights, scale bytes
     const int x0 = from * 128, w0 = MODE == kA16W4 ? from * 32 : from * 128, s0 = from * (MODE == kFp4 ? 8 : 2);
+    // rows outside x are read as its first (last, without x_perm) one
+    const int x_first = a.x_perm ? 0 : min(t.row0, a.x_rows - 1);
     auto x_at = [&](int r) {
       const int m = min(r, t.nrows - 1), i = t.row0 + m;
-      return max(x_row(a, i, a.perm ? perm[m] : i), 0);
+      return a.x_perm ? max(x_row(a, i, perm[m]), 0) : min(i, a.x_rows - 1) - x_first;
     };
     const int n_out = a.swiglu ? a.N / 2 : a.N, c0 = t.nb * (a.swiglu ? HN : S::BN);
     const int64_t K = a.K;
@@ -590,6 +603,7 @@ struct WideSource {
       return a.swiglu ? min(c0 + r % HN, n_out - 1) + (r >= HN ? n_out : 0) : min(c0 + r, n_out - 1);
     };
     wbase = a.w + (int64_t)t.entry * a.N * wrow_b;
+    xbase = a.x + (int64_t)x_first * xrow_b;
 #pragma unroll
     for (int q = 0; q < WQ; ++q) w[q] = w_row(q * RQ + (tid >> 3)) * wrow_b + w0 + ch * 16;
 #pragma unroll
@@ -598,7 +612,7 @@ struct WideSource {
 #pragma unroll
       for (int q = 0; q < SQ; ++q) {
         const int r = q * T + tid;
-        if (MODE == kFp4 && r >= S::BN) s[q] = a.xs + (int64_t)x_at(r - S::BN) * (K / 32) + s0;
+        if (MODE == kFp4 && r >= S::BN) s[q] = a.xs + ((int64_t)x_first + x_at(r - S::BN)) * (K / 32) + s0;
         else s[q] = a.ws + ((int64_t)t.entry * a.N + w_row(min(r, S::BN - 1))) * (K / 32) + s0;
       }
     }
@@ -661,9 +675,9 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
   auto request_x = [&](int s, int at, int q) {
     const uint32_t dst = xdst + (((s + at) & 1) * S::BM + q * RQ) * 128;
     if ((s + 1) * 128 <= xb)
-      load_lds16(a.x + s * 128, src.x[q], dst);
+      load_lds16(src.xbase + s * 128, src.x[q], dst);
     else
-      load_lds16(a.x, src.x[q] + (s * 128 + ch * 16 < xb ? s * 128 : -(uint32_t)(ch * 16)), dst);
+      load_lds16(src.xbase, src.x[q] + (s * 128 + ch * 16 < xb ? s * 128 : -(uint32_t)(ch * 16)), dst);
   };
 
   f32x4_t acc[NF][MF];
@@ -776,7 +790,7 @@ __device__ __forceinline__ void wide_tile(const ProductArgs& a, int n_nb, WideLd
     // wait for it, and so for the stage on its way, before this stage's products.
     if (KG == 1 && s == 0 && more) {
       next_tile<S::BM>(a, b, total, n_nb, all.first, &next);
-      if (a.perm && wave * 64 < S::BM)
+      if (a.x_perm && wave * 64 < S::BM)
         load_lds4(a.perm + next.row0 + min(tid, next.nrows - 1), pdst);
     }
     if (KG == 1 && last && more) {
@@ -908,7 +922,7 @@ product_wide_kernel(ProductArgs a, int n_nb) {
       load_lds16(src.wbase, src.w[q] - (ch * 16 < wb ? 0 : ch * 16), wdst + q * RQ * 128);
 #pragma unroll
     for (int q = 0; q < S::BM / RQ; ++q)
-      if (q * RQ < t.nrows) load_lds16(a.x, src.x[q] - (ch * 16 < xb ? 0 : ch * 16), xdst + q * RQ * 128);
+      if (q * RQ < t.nrows) load_lds16(src.xbase, src.x[q] - (ch * 16 < xb ? 0 : ch * 16), xdst + q * RQ * 128);
   }
   __builtin_amdgcn_s_waitcnt((7 << 4) | (15 << 8));
   asm volatile("" ::: "memory");
@@ -960,7 +974,9 @@ int launch_few(const ProductArgs& a, hipStream_t s) {
   MC_REQUIRE(tiles <= 0x7FFF0000, "product of %d rows with %d columns is too large", a.M, a.N);
   const int steps = WF == MC_BF16 ? a.K / 32 : (a.K + 127) / 128;
   auto run = [&](auto kernel, int kw) {
-    hipLaunchKernelGGL(kernel, dim3((unsigned)tiles), dim3(64 * nt * kw), 0, s, a, (int)n_nb);
+    const int64_t most = UINT32_MAX / (64 * nt * kw);
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(tiles < most ? tiles : most)), dim3(64 * nt * kw), 0, s, a, (int)n_nb,
+                       (uint32_t)tiles);
   };
   // Waves along K x steps in flight per wave: loads of steps past the end cost what others do, so both
   // follow K (one token 4096 x 2048 4.5 us in 8 x 2, 5.8 in 8 x 4, 4.6 in 16 x 1; 8 x 8192 x 2048 7.1 /
@@ -1012,10 +1028,10 @@ int launch_by_size(const ProductArgs& a, hipStream_t s) {
   typedef WideShape<2, 2, 4, 4, 2, 1> Medium2;    // 128 x 128, K in two parts
   typedef WideShape<2, 1, 4, 2, 2, 2> Small2;     // 64 x 64, K in two parts, two per CU
   typedef WideShape<2, 1, 4, 2, 4, 1> Small4;     // 64 x 64, K in four parts
-  // bytes of a matrix and of x, which the wide kernels reach with 32-bit offsets (beyond, the tiles
-  // of 16 rows read with 64-bit ones)
+  // bytes of a matrix and of x (of a tile's rows of it, if they lie one behind the other), which the
+  // wide kernels reach with 32-bit offsets (beyond, the tiles of 16 rows read with 64-bit ones)
   const int64_t w_bytes = (int64_t)a.N * (a.w_fmt == MC_BF16 ? 2 * (int64_t)a.K : a.K / 2);
-  const int64_t x_bytes = a.x_rows * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
+  const int64_t x_bytes = (a.x_perm ? a.x_rows : Big::BM) * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
   // Up to 16 rows: one token's experts 8 us (12 in Small4), 8 x 4096 x 4096 7 us (16); from 17 rows on
   // Small4 is level or ahead (17 x 4096 x 2048 bf16: 8 against 12 us, 64 x 4096 x 4096: 19 against
   // 35 us).

@@ -417,6 +417,50 @@ def test_rows_beyond_32_bit_offsets(xf, wf):
     gpu_check(y[7:], x64[7:], w64[1], False, F32, xf)
 
 
+@pytest.mark.parametrize("xf,wf", FORMATS)
+def test_consecutive_rows_beyond_32_bit_offsets(xf, wf):
+    """All rows of an x of more than 4 GiB, one behind the other."""
+    K, N = 8192, 32
+    M = (1 << 32) // (2 * K if xf == "bf16" else K // 2) + 300
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    at = torch.tensor([0, 5, 4000, M // 2] + list(range(M - 290, M - 10)) + [M - 1], device="cuda")
+    part, ps, x64 = gpu_operand(g, xf, len(at), K)
+    x = torch.zeros((M, part.shape[1]), dtype=part.dtype, device="cuda")
+    x[at] = part
+    xs = None
+    if ps is not None:
+        xs = torch.zeros((M, K // 32), dtype=U8, device="cuda")
+        xs[at] = ps
+    w, ws, w64 = gpu_operand(g, wf, 2, N, K, size=2.0 ** -5)
+    y = torch.empty((M, N), dtype=F32, device="cuda")
+    cut = M - 150
+    mc.grouped_matmul(x, w, torch.tensor([0, cut, M], dtype=I32, device="cuda"), y, x_scale=xs, w_scale=ws)
+    lo = at < cut
+    gpu_check(y[at[lo]], x64[lo], w64[0], False, F32, xf)
+    gpu_check(y[at[~lo]], x64[~lo], w64[1], False, F32, xf)
+    if wf == "mxfp4":
+        mc.mxfp4_matmul(x, w[0], ws[0], y, x_scale=xs)
+        gpu_check(y[at], x64, w64[0], False, F32, xf)
+
+
+def test_more_columns_than_a_launch_holds():
+    """One token and so many columns that workgroups take several tiles."""
+    N, K = (1 << 28) + 1100, 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    x, _, x64 = gpu_operand(g, "bf16", 1, K)
+    at = torch.tensor([0, 1, N // 2] + list(range((1 << 28) - 100, N)), device="cuda")
+    part, ps, w64 = gpu_operand(g, "mxfp4", len(at), K)
+    w = torch.zeros((N, K // 2), dtype=U8, device="cuda")
+    ws = torch.full((N, 1), 127, dtype=U8, device="cuda")
+    w[at], ws[at] = part, ps
+    y = torch.full((1, N), float("nan"), dtype=F32, device="cuda")
+    mc.mxfp4_matmul(x, w, ws, y)
+    gpu_check(y[:, at], x64, w64, False, F32, "")
+    assert int((y != 0).sum()) <= len(at)          # every other column was written with its 0
+
+
 def test_grouped_entries_and_bad_rows():
     """entry_of leaves groups out or maps them to other matrices; entries, routes and offsets outside
     their ranges skip rows and touch nothing."""
