@@ -450,9 +450,10 @@ def _codes(fn: str, what: str, codes, scales) -> int:
     if _torch is None:
         _load_torch()
     u8 = _torch.uint8
-    shape = codes.shape
-    if (codes.dtype != u8 or scales.dtype != u8 or not codes.is_contiguous() or not scales.is_contiguous()
-            or scales.shape[:-1] != shape[:-1] or scales.shape[-1] * 16 != shape[-1]):
+    shape, blocks = codes.shape, scales.shape
+    if (codes.dtype is not u8 or scales.dtype is not u8 or not codes.is_contiguous() or not scales.is_contiguous()
+            or len(shape) != len(blocks) or blocks[-1] * 16 != shape[-1]
+            or (blocks[0] != shape[0] if len(shape) == 2 else blocks[:-1] != shape[:-1])):
         raise ValueError("%s: %s must be contiguous uint8 codes [..., C/2] with scales [..., C/32], not %s %s and %s %s"
                          % (fn, what, codes.dtype, tuple(shape), scales.dtype, tuple(scales.shape)))
     return 2 * shape[-1]
