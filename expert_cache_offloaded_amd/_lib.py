@@ -17,7 +17,10 @@ LIB_PATH = os.path.join(HERE, "libmc.so")
 MC_OK, MC_EINVAL, MC_ENOMEM, MC_EHIP, MC_EUNSUPPORTED, MC_EDEVICE = 0, -1, -2, -3, -4, -5
 MC_BF16, MC_MXFP4, MC_F32, MC_F16 = 0, 1, 2, 3
 MC_SPLIT_SUBMIT, MC_MERGE = 0, 1
+MC_MXFP4_F32 = 4
 FMT = {"bf16": MC_BF16, "mxfp4": MC_MXFP4}
+# activations of a prefill layer (moe_experts_prefill_act)
+ACT = {"bf16": MC_BF16, "mxfp4": MC_MXFP4, "mxfp4_f32": MC_MXFP4_F32}
 STAT_NAMES = ("hits", "misses", "fills", "host", "evictions", "calls", "err", "reserved")
 
 
@@ -569,13 +572,13 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
 
 
 def prefill_act_ws_bytes(T: int, k: int, E: int, H: int, I: int, act: str) -> int:
-    return int(lib().moe_experts_prefill_act_ws_bytes(T, k, E, H, I, FMT[act]))
+    return int(lib().moe_experts_prefill_act_ws_bytes(T, k, E, H, I, ACT[act]))
 
 
 def _layer_device(fn: str, x, ids, w, n_tok, H: int, act: str, ws, y, *rest) -> int:
     """Checks the tensors of a prefill layer call; the GPU they are on."""
-    if act not in FMT:
-        raise ValueError("%s: act must be bf16 or mxfp4, not %r" % (fn, act))
+    if act not in ACT:
+        raise ValueError("%s: act must be bf16, mxfp4 or mxfp4_f32, not %r" % (fn, act))
     if _torch is None:
         _load_torch()
     if ids.dim() != 2:
@@ -596,14 +599,15 @@ def _layer_device(fn: str, x, ids, w, n_tok, H: int, act: str, ws, y, *rest) -> 
 
 def moe_experts_prefill_act(x, ids, w, n_tok, E: int, layer_buf: Banks, act: str, ws, y,
                             nxt: Optional[Prefetch] = None, stream=None) -> None:
-    """Prefill layer on bf16 or MXFP4 activations (act = "bf16" or "mxfp4"): x and y bf16 (values or
-    bits) [T][H], ids int32 and w fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes."""
+    """Prefill layer on bf16 or MXFP4 activations: x and y bf16 (values or bits) [T][H], ids int32 and w
+    fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes.  act: "bf16", "mxfp4" (each route's
+    output rounded to bf16 before the sum over routes) or "mxfp4_f32" (kept in fp32)."""
     fn = "moe_experts_prefill_act"
     d = _layer_device(fn, x, ids, w, n_tok, layer_buf.H, act, ws, y)
     T, k = ids.shape
     f = lib().moe_experts_prefill_act
     _call(fn, d, stream, lambda st: f(
-        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(layer_buf), FMT[act], ws.data_ptr(),
+        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(layer_buf), ACT[act], ws.data_ptr(),
         ws.numel() * ws.element_size(), y.data_ptr(), st, C.byref(nxt) if nxt is not None else None))
 
 
@@ -618,7 +622,7 @@ def moe_experts_prefill_act_part(x, ids, w, n_tok, E: int, part_buf: Banks, entr
             _packed(fn, what, t, (E,), _torch.int32)
     f = lib().moe_experts_prefill_act_part
     _call(fn, d, stream, lambda st: f(
-        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(part_buf), _ptr(entry_of), FMT[act],
+        x.data_ptr(), ids.data_ptr(), w.data_ptr(), T, k, _ptr(n_tok), E, C.byref(part_buf), _ptr(entry_of), ACT[act],
         steps, ws.data_ptr(), ws.numel() * ws.element_size(), _ptr(counts), _ptr(y), st))
 
 

@@ -7,10 +7,10 @@
 // epilogue multiplies by the gate and scatters each route to its own row of a [T*k][H] buffer
 // (no atomics); the sum of each token's routes in route order, in fp32, rounded once.
 //
-// The route outputs are fp32 for bf16 activations and bf16 for MXFP4 ones: there the quantised x
-// and h are off by 0.1 and more, a bf16 rounding by at most 2^-8, and the buffer's write and read,
-// 805 MB each way at 8192 tokens x 6 routes x 4096 in fp32, are a quarter of the layer's traffic
-// (layer 1.37 ms with fp32 outputs, 1.27 with bf16).
+// The route outputs are fp32, but for act MC_MXFP4, whose caller asked for the shorter buffer: its
+// write and read, 805 MB each way at 8192 tokens x 6 routes x 4096 in fp32, are a quarter of the
+// layer's traffic (layer 1.37 ms with fp32 outputs, 1.27 with bf16).  Each route is then off by up to
+// 2^-8 of itself, which makes the rounding error of y about 1.4 times as large (rms, six routes).
 #include "prefill.h"
 #include "product.h"
 
@@ -22,8 +22,12 @@ struct ActWs {
   SortBuffers sort;
   uint8_t *xq, *xqs;          // MXFP4 x: [T][H/2], [T][H/32]
   uint8_t *h, *hs;            // sorted rows of h: bf16 [T*k][I], or MXFP4 codes and scales
-  void* yr;                   // gated route outputs [T*k][H]: fp32, or bf16 (MXFP4 activations)
+  void* yr;                   // gated route outputs [T*k][H]: fp32, or bf16 (bf16_routes)
 };
+
+// The format of an act's activations, and whether its route outputs are bf16.
+static int act_fmt(int act) { return act == MC_MXFP4_F32 ? MC_MXFP4 : act; }
+static bool bf16_routes(int act) { return act == MC_MXFP4; }
 
 static size_t ws_layout(int T, int k, int E, int H, int I, int act, ActWs* w, uint8_t* base) {
   size_t o = 0;
@@ -39,7 +43,7 @@ static size_t ws_layout(int T, int k, int E, int H, int I, int act, ActWs* w, ui
   v.sort.offsets = (int32_t*)take((size_t)(E + 1) * 4);
   v.sort.mtile_off = (int32_t*)take((size_t)(E + 1) * 4);
   v.sort.perm = (int32_t*)take(nr * 4);
-  if (act == MC_MXFP4) {
+  if (act_fmt(act) == MC_MXFP4) {
     v.xq = take((size_t)T * H / 2);
     v.xqs = take((size_t)T * H / 32);
     v.h = take(nr * I / 2);
@@ -47,7 +51,7 @@ static size_t ws_layout(int T, int k, int E, int H, int I, int act, ActWs* w, ui
   } else {
     v.h = take(nr * I * 2);
   }
-  v.yr = take(nr * H * (act == MC_MXFP4 ? 2 : 4));
+  v.yr = take(nr * H * (bf16_routes(act) ? 2 : 4));
   if (w) *w = v;
   return o;
 }
@@ -98,7 +102,7 @@ act_combine_kernel(const int32_t* __restrict__ ids, int T, int k, int E, int H, 
 using namespace mc;
 
 extern "C" size_t moe_experts_prefill_act_ws_bytes(int32_t T, int32_t k, int32_t E, int32_t H, int32_t I, int32_t act) {
-  if (T < 0 || k < 0 || E < 0 || H < 0 || I < 0 || (act != MC_BF16 && act != MC_MXFP4)) return 0;
+  if (T < 0 || k < 0 || E < 0 || H < 0 || I < 0 || (act != MC_BF16 && act != MC_MXFP4 && act != MC_MXFP4_F32)) return 0;
   return ws_layout(T, k, E, H, I, act, nullptr, nullptr);
 }
 
@@ -107,7 +111,7 @@ static int check_args(const char* fn, const void* x, const int32_t* ids, const f
                       bool need_y) {
   int rc;
   if ((rc = check_banks(buf, fn)) != MC_OK) return rc;
-  MC_REQUIRE(act == MC_BF16 || act == MC_MXFP4, "%s: activations of format %d", fn, act);
+  MC_REQUIRE(act == MC_BF16 || act == MC_MXFP4 || act == MC_MXFP4_F32, "%s: activations of format %d", fn, act);
   MC_REQUIRE(act == MC_BF16 || buf->fmt == MC_MXFP4, "%s: MXFP4 activations need MXFP4 experts", fn);
   MC_REQUIRE(T >= 0 && k >= 1 && E >= 1 && E <= kP_MaxE && k <= E, "%s: T=%d k=%d E=%d", fn, T, k, E);
   // the products' limits (check_product)
@@ -126,14 +130,14 @@ static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int
                      int32_t E, const mc_banks* buf, const int32_t* entry_of, int32_t act, int32_t steps, void* ws,
                      int32_t* counts, void* y_bf16, hipStream_t s) {
   int rc;
-  const int H = buf->H, I = buf->I;
+  const int H = buf->H, I = buf->I, fmt = act_fmt(act);
   ActWs v{};
   ws_layout(T, k, E, H, I, act, &v, static_cast<uint8_t*>(ws));
   if (steps & MC_PF_SORT) {
     // the counts go straight to the caller's array, if there is one
     if (counts) v.sort.counts = counts;
     if ((rc = sort_routes_launch(ids, T, k, n_tok, E, v.sort, s)) != MC_OK) return rc;
-    if (act == MC_MXFP4 && (rc = mc_mxfp4_quantize(x_bf16, MC_BF16, T, H, H, v.xq, v.xqs, s)) != MC_OK) return rc;
+    if (fmt == MC_MXFP4 && (rc = mc_mxfp4_quantize(x_bf16, MC_BF16, T, H, H, v.xq, v.xqs, s)) != MC_OK) return rc;
   }
   if (steps & MC_PF_EXPERTS) {
     ProductArgs p{};
@@ -143,10 +147,10 @@ static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int
     p.offsets = v.sort.offsets;
     p.perm = v.sort.perm;
     p.entry_of = entry_of;
-    p.x_fmt = act;
+    p.x_fmt = fmt;
     p.w_fmt = buf->fmt;
     // h = silu(x W_gate^T) * (x W_up^T), rows in sorted order
-    p.x = act == MC_MXFP4 ? v.xq : static_cast<const uint8_t*>(x_bf16);
+    p.x = fmt == MC_MXFP4 ? v.xq : static_cast<const uint8_t*>(x_bf16);
     p.xs = v.xqs;
     p.ldx = H;
     p.x_rows = T;
@@ -159,7 +163,7 @@ static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int
     p.swiglu = 1;
     p.y = v.h;
     p.ys = v.hs;
-    p.y_fmt = act;
+    p.y_fmt = fmt;
     p.ldy = I;
     p.y_rows = T * k;
     if ((rc = launch_product(p, s)) != MC_OK) return rc;
@@ -176,7 +180,7 @@ static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int
     p.swiglu = 0;
     p.y = static_cast<uint8_t*>(v.yr);
     p.ys = nullptr;
-    p.y_fmt = act == MC_MXFP4 ? MC_BF16 : MC_F32;
+    p.y_fmt = bf16_routes(act) ? MC_BF16 : MC_F32;
     p.ldy = H;
     p.y_perm = 1;
     p.gate = w;
@@ -184,7 +188,7 @@ static int act_steps(const void* x_bf16, const int32_t* ids, const float* w, int
     if ((rc = launch_product(p, s)) != MC_OK) return rc;
   }
   if (steps & MC_PF_COMBINE) {
-    if (act != MC_MXFP4)
+    if (!bf16_routes(act))
       return combine_launch(ids, T, k, E, H, n_tok, static_cast<const float*>(v.yr), static_cast<uint16_t*>(y_bf16), s);
     const int64_t blocks = ((int64_t)T * (H / 8) + 255) / 256;
     hipLaunchKernelGGL(act_combine_kernel, dim3((unsigned)(blocks < 16384 ? blocks : 16384)), dim3(256), 0, s, ids, T, k, E,

@@ -295,10 +295,10 @@ class PrefillRunner:
     After the last layer the experts left in the buffers are installed in the cache
     (mc_cache_install on the freshly reset tables).
 
-    act chooses the activations of the layers: "mxfp4" (MXFP4 experts; x and h quantised,
-    moe_experts_prefill_act) or "bf16" (either format, h rounded to bf16); by default MXFP4
-    experts run on bf16 activations with h in fp16 (moe_experts_prefill), bf16 experts on
-    "bf16"."""
+    act chooses the activations of the layers: "mxfp4" or "mxfp4_f32" (MXFP4 experts; x and h
+    quantised, route outputs held in bf16 or in fp32, moe_experts_prefill_act) or "bf16"
+    (either format, h rounded to bf16); by default MXFP4 experts run on bf16 activations with
+    h in fp16 (moe_experts_prefill), bf16 experts on "bf16"."""
 
     def __init__(self, cache: "CacheState", host: "BankSet", pool: "BankSet", T: int, k: int,
                  act: Optional[str] = None):
@@ -307,8 +307,8 @@ class PrefillRunner:
             raise ValueError("prefill needs at least one slot")
         if act is None and pool.fmt == "bf16":
             act = "bf16"
-        if act not in (None, "bf16", "mxfp4") or (act == "mxfp4" and pool.fmt != "mxfp4"):
-            raise ValueError("act must be bf16, mxfp4 (with MXFP4 experts) or None, not %r" % (act,))
+        if act not in (None, *L.ACT) or (act not in (None, "bf16") and pool.fmt != "mxfp4"):
+            raise ValueError("act must be bf16, mxfp4 or mxfp4_f32 (with MXFP4 experts) or None, not %r" % (act,))
         self.cache, self.host, self.pool, self.T, self.k, self.act = cache, host, pool, T, k, act
         self.double = pool.n >= 2 * E
         dev = pool.t["gate_up"].device
