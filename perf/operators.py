@@ -308,9 +308,11 @@ def _own(s):
                           x_div=c["k"], y_perm=c["gate"], gate=s["gates"], swiglu=c["swiglu"])
     else:
         banks = mc.make_banks("mxfp4" if c["act"] == "mxfp4" else "bf16", c["H"], c["I"], s["banks"])
-        ws = torch.empty(mc.prefill_act_ws_bytes(c["T"], c["k"], c["E"], c["H"], c["I"], c["act"]),
+        # the plain form's route outputs are not rounded before their sum
+        act = "mxfp4_f32" if c["act"] == "mxfp4" else "bf16"
+        ws = torch.empty(mc.prefill_act_ws_bytes(c["T"], c["k"], c["E"], c["H"], c["I"], act),
                          dtype=torch.uint8, device=DEV)
-        mc.moe_experts_prefill_act(s["x"], s["ids"], s["gates"], s["n_tok"], c["E"], banks, c["act"], ws, y)
+        mc.moe_experts_prefill_act(s["x"], s["ids"], s["gates"], s["n_tok"], c["E"], banks, act, ws, y)
     return y
 
 
