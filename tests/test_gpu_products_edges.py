@@ -1,0 +1,62 @@
+"""Products at the edges of their inputs."""
+import numpy as np
+import pytest
+import torch
+
+import expert_cache_offloaded_amd as mc
+from oracle import decode_mxfp4
+from test_gpu_products import BF, F32, FORMATS, I32, U8, dev, silu64, swiglu_bound
+
+pytestmark = pytest.mark.gpu
+
+MAGNITUDES = [6.0, 4.0, 3.0, 2.0, 1.5, 1.0, 0.5]      # e2m1 codes 7 .. 1
+
+
+def codes_with_sum(total):
+    """32 e2m1 codes whose values add up to `total` (a multiple of 0.5)."""
+    codes, left = [], abs(total)
+    for i, m in enumerate(MAGNITUDES):
+        while left >= m and len(codes) < 32:
+            codes.append(7 - i + (8 if total < 0 else 0))
+            left -= m
+    assert left == 0
+    return codes + [0] * (32 - len(codes))
+
+
+def pack(rows):
+    c = np.array(rows, dtype=np.uint8)
+    return c[:, 0::2] | (c[:, 1::2] << 4)
+
+
+@pytest.mark.parametrize("xf,wf", FORMATS)
+@pytest.mark.parametrize("M", [3, 70, 300])
+def test_swiglu_of_large_gates(xf, wf, M):
+    """Gates down to -88.5, where e^-g is near fp32's end and silu(g) = g / (1 + e^-g), about 1e-37,
+    still a normal number, with up values that bring it back to size; and up to 100, where silu(g) = g."""
+    gates = [-88.5, -88.0, -87.5, -87.0, -80.0, -60.0, -20.0, -1.0, 0.0, 1.0, 20.0, 100.0]
+    n = 32
+    g = [gates[i % len(gates)] for i in range(n)]
+    up = [1.0 + 0.5 * (i % 5) for i in range(n)]
+    codes = pack([codes_with_sum(v) for v in g + up])
+    scales = np.full((2 * n, 1), 127, dtype=np.uint8)
+    scales[n:] = 127 + 60
+    w64 = decode_mxfp4(codes, scales)
+    x64 = np.ones((M, 32))
+    if xf == "bf16":
+        x, xs = torch.ones((M, 32), dtype=BF, device="cuda"), None
+    else:
+        x = torch.full((M, 16), 0x22, dtype=U8, device="cuda")
+        xs = torch.full((M, 1), 127, dtype=U8, device="cuda")
+    if wf == "bf16":
+        w, ws = torch.from_numpy(w64).to(BF).cuda()[None], None
+    else:
+        w, ws = dev(codes)[None], dev(scales)[None]
+    y = torch.full((M, n), 7.0, dtype=F32, device="cuda")
+    mc.grouped_matmul(x, w, torch.tensor([0, M], dtype=I32, device="cuda"), y, x_scale=xs, w_scale=ws, swiglu=True)
+    # the sums are exact: multiples of half a unit below 2^24 of them
+    v = x64 @ w64.T
+    ref = silu64(v[:, :n]) * v[:, n:]
+    tol = swiglu_bound(v, np.zeros_like(v), n) + 2.0 ** -24 * np.abs(ref)
+    off = np.abs(y.double().cpu().numpy() - ref)
+    bad = ~(off <= tol)
+    assert not bad.any(), (sorted(set(np.array(g)[np.nonzero(bad)[1]])), np.max(off[bad] / np.abs(ref[bad])))
