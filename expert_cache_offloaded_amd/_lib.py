@@ -564,10 +564,13 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
     if x_perm is None:
         x_perm = perm is not None
     d = _device(fn, x, w, offsets, y, x_scale, w_scale, y_scale, perm, gate, entry_of)
+    # the address of a tensor without elements is null, which would stand for no gates at all (of no
+    # gates none is read)
+    gates = _ptr(gate) if gate is None or gate.numel() else offsets.data_ptr()
     g = Grouped(xf, wf, yf, 1 if swiglu else 0, E, M, N, K, x.shape[0], x_div, rows, 1 if x_perm else 0,
                 1 if y_perm else 0, 0 if gate is None else gate.numel(), ldx, ldy, n, x.data_ptr(), _ptr(x_scale),
                 w.data_ptr(), _ptr(w_scale), y.data_ptr(), _ptr(y_scale), offsets.data_ptr(), _ptr(perm),
-                _ptr(entry_of), _ptr(gate))
+                _ptr(entry_of), gates)
     _call("mc_grouped_matmul", d, stream, lib().mc_grouped_matmul, C.byref(g))
 
 

@@ -60,3 +60,20 @@ def test_swiglu_of_large_gates(xf, wf, M):
     off = np.abs(y.double().cpu().numpy() - ref)
     bad = ~(off <= tol)
     assert not bad.any(), (sorted(set(np.array(g)[np.nonzero(bad)[1]])), np.max(off[bad] / np.abs(ref[bad])))
+
+
+@pytest.mark.parametrize("wf", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("M", [5, 90])
+def test_gates_of_no_rows_skip_every_row(wf, M):
+    """Rows past the gates' end are skipped; where there is no gate at all that is every row, whichever
+    way the empty tensor came about."""
+    n, K = 64, 64
+    x = torch.ones((M, K), dtype=BF, device="cuda")
+    w = torch.ones((1, n, K), dtype=BF, device="cuda") if wf == "bf16" else torch.full((1, n, K // 2), 0x22, dtype=U8, device="cuda")
+    ws = None if wf == "bf16" else torch.full((1, n, K // 32), 127, dtype=U8, device="cuda")
+    off = torch.tensor([0, M], dtype=I32, device="cuda")
+    for some, rows in ((torch.ones(M, device="cuda")[:0], 0), (torch.empty(0, device="cuda"), 0),
+                       (torch.ones(3, device="cuda"), 3)):
+        y = torch.full((M, n), 7.0, dtype=F32, device="cuda")
+        mc.grouped_matmul(x, w, off, y, w_scale=ws, gate=some)
+        assert (y[:rows] == K).all() and (y[rows:] == 7.0).all()
