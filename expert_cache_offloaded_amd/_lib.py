@@ -411,6 +411,12 @@ def _device(fn: str, first, *rest) -> int:
     return d
 
 
+def _int32(fn: str, *sizes) -> None:
+    """Refuses sizes that a 32-bit argument would cut to other ones."""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise ValueError("%s: sizes %s do not fit in 32 bits" % (fn, sizes))
+
+
 def _call(name: str, device: int, stream, fn, *args) -> None:
     """fn(*args, stream handle) with the tensors' GPU current, on the given stream or on that GPU's
     current one."""
@@ -510,6 +516,7 @@ def mxfp4_matmul(x, w, w_scale, y, x_scale=None, stream=None) -> None:
     M, N = x.shape[0], w.shape[0]
     xf, ldx = _x_operand(fn, x, x_scale, K)
     ldy = _rows(fn, "y", y, N, M)
+    _int32(fn, M, N, K)
     _call("mc_mxfp4_matmul", _device(fn, x, w, w_scale, y, x_scale), stream, lib().mc_mxfp4_matmul, x.data_ptr(),
           _ptr(x_scale), xf, ldx, w.data_ptr(), w_scale.data_ptr(), M, N, K, y.data_ptr(), _etype(y), ldy)
 
@@ -563,18 +570,21 @@ def grouped_matmul(x, w, offsets, y, x_scale=None, w_scale=None, y_scale=None, s
         _packed(fn, "gate", gate, gate.shape, _torch.float32)
     if x_perm is None:
         x_perm = perm is not None
+    n_gate = 0 if gate is None else gate.numel()
+    _int32(fn, E, M, N, K, x.shape[0], x_div, rows, n_gate)
     d = _device(fn, x, w, offsets, y, x_scale, w_scale, y_scale, perm, gate, entry_of)
     # the address of a tensor without elements is null, which would stand for no gates at all (of no
     # gates none is read)
-    gates = _ptr(gate) if gate is None or gate.numel() else offsets.data_ptr()
+    gates = _ptr(gate) if gate is None or n_gate else offsets.data_ptr()
     g = Grouped(xf, wf, yf, 1 if swiglu else 0, E, M, N, K, x.shape[0], x_div, rows, 1 if x_perm else 0,
-                1 if y_perm else 0, 0 if gate is None else gate.numel(), ldx, ldy, n, x.data_ptr(), _ptr(x_scale),
+                1 if y_perm else 0, n_gate, ldx, ldy, n, x.data_ptr(), _ptr(x_scale),
                 w.data_ptr(), _ptr(w_scale), y.data_ptr(), _ptr(y_scale), offsets.data_ptr(), _ptr(perm),
                 _ptr(entry_of), gates)
     _call("mc_grouped_matmul", d, stream, lib().mc_grouped_matmul, C.byref(g))
 
 
 def prefill_act_ws_bytes(T: int, k: int, E: int, H: int, I: int, act: str) -> int:
+    _int32("prefill_act_ws_bytes", T, k, E, H, I)
     return int(lib().moe_experts_prefill_act_ws_bytes(T, k, E, H, I, ACT[act]))
 
 
@@ -606,6 +616,7 @@ def moe_experts_prefill_act(x, ids, w, n_tok, E: int, layer_buf: Banks, act: str
     fp32 [T][k], n_tok int32 [1] or None, ws of prefill_act_ws_bytes.  act: "bf16", "mxfp4" (each route's
     output rounded to bf16 before the sum over routes) or "mxfp4_f32" (kept in fp32)."""
     fn = "moe_experts_prefill_act"
+    _int32(fn, E, *ids.shape)
     d = _layer_device(fn, x, ids, w, n_tok, layer_buf.H, act, ws, y)
     T, k = ids.shape
     f = lib().moe_experts_prefill_act
@@ -618,6 +629,7 @@ def moe_experts_prefill_act_part(x, ids, w, n_tok, E: int, part_buf: Banks, entr
                                  counts=None, y=None, stream=None) -> None:
     """One or more steps of that layer (PF_SORT / PF_EXPERTS / PF_COMBINE) on ws."""
     fn = "moe_experts_prefill_act_part"
+    _int32(fn, E, steps, *ids.shape)
     d = _layer_device(fn, x, ids, w, n_tok, part_buf.H, act, ws, y, entry_of, counts)
     T, k = ids.shape
     for what, t in (("entry_of", entry_of), ("counts", counts)):
