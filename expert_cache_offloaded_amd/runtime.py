@@ -69,7 +69,7 @@ def quantize_banks(src: BankSet, dst: BankSet, device="cuda") -> None:
                          % ((src.n, src.H, src.I), (dst.n, dst.H, dst.I)))
     for name in ("gate_up", "down"):
         s, codes, scales = src.t[name], dst.t[name], dst.t[name + "_scale"]
-        step = max(1, (64 << 20) // (s[0].numel() * 2))
+        step = max(1, (64 << 20) // (s.shape[1] * s.shape[2] * 2))
         for i in range(0, src.n, step):
             j = min(i + step, src.n)
             rows, cols = (j - i) * s.shape[1], s.shape[2]

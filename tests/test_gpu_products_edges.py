@@ -77,3 +77,10 @@ def test_gates_of_no_rows_skip_every_row(wf, M):
         y = torch.full((M, n), 7.0, dtype=F32, device="cuda")
         mc.grouped_matmul(x, w, off, y, w_scale=ws, gate=some)
         assert (y[:rows] == K).all() and (y[rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("where", ["cpu", "cuda"])
+def test_quantize_banks_of_no_experts(where):
+    from expert_cache_offloaded_amd.runtime import BankSet, alloc_banks, quantize_banks
+    a, b = (BankSet(alloc_banks(0, 128, 64, f, device=where), 128, 64, f) for f in ("bf16", "mxfp4"))
+    quantize_banks(a, b)
