@@ -459,8 +459,9 @@ int mc_mxfp4_quantize(const void* src, int32_t type, int64_t rows, int64_t cols,
 
 /*
  * The values of MXFP4 rows: dst = e2m1(code) * 2^(X - 127), rounded once to `type` (bf16 and
- * fp32 hold every value down to their subnormals' last bit; fp16 overflows to infinity and
- * rounds below 2^-24).  X = 255 gives NaN.  Layout and limits as mc_mxfp4_quantize, dst
+ * fp32 hold every value below 2^128; larger ones, of X = 253 and 254, which the quantiser
+ * does not write, become infinity; fp16 overflows to infinity and rounds below 2^-24).
+ * X = 255 gives NaN.  Layout and limits as mc_mxfp4_quantize, dst
  * rows ld elements apart; the elements between a row's end and the next row are left as
  * they are.
  */
@@ -474,9 +475,12 @@ int mc_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int
  *   w, w_scale  device MXFP4 [N][K/2], [N][K/32]
  *   y    device, y_fmt MC_BF16 or MC_F32, [M] rows ldy elements apart (ldy >= N)
  * x, w and y are 16-byte aligned, scales have any alignment.  Products are exact and summed
- * in fp32 (the order depends on sizes and alignment only), each result is rounded once.  K % 32 == 0,
- * 32 <= K <= 2^28; M and N up to 2^31 - 2^16; M = 0 or N = 0 enqueues nothing.  A NaN scale makes the results that read it NaN.
- * y may not overlap an input.
+ * in fp32 (the order depends on sizes and alignment only), each result is rounded once.  With
+ * bf16 x the weights become bf16 first: those of 2^128 and more (X = 253 with magnitudes 4 and
+ * 6, X = 254 with 2 and up, which the quantiser does not write) become infinity; MXFP4 x
+ * multiplies them as they are.  K % 32 == 0, 32 <= K <= 2^28; M and N up to 2^31 - 2^16; M = 0
+ * or N = 0 enqueues nothing.  A NaN scale makes the results that read it NaN.  y may not
+ * overlap an input.
  */
 int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt, int64_t ldx, const void* w,
                     const void* w_scale, int32_t M, int32_t N, int32_t K, void* y, int32_t y_fmt,

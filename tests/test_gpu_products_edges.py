@@ -5,7 +5,7 @@ import torch
 
 import expert_cache_offloaded_amd as mc
 from oracle import decode_mxfp4
-from test_gpu_products import BF, F32, FORMATS, I32, U8, dev, silu64, swiglu_bound
+from test_gpu_products import BF, F32, FORMATS, I32, U8, dev, product_bound, silu64, swiglu_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -77,6 +77,43 @@ def test_gates_of_no_rows_skip_every_row(wf, M):
         y = torch.full((M, n), 7.0, dtype=F32, device="cuda")
         mc.grouped_matmul(x, w, off, y, w_scale=ws, gate=some)
         assert (y[:rows] == K).all() and (y[rows:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M", [3, 70, 300])
+def test_largest_scales(M):
+    """Weights with the scale bytes 253 and 254, whose larger codes stand for 2^128 and more.  Times MXFP4
+    rows they are applied inside the matrix instruction and the products come out; times bf16 rows
+    the weight becomes a bf16 first, and those codes infinity."""
+    rng = np.random.default_rng(M)
+    N, K = 40, 64
+    for X, largest in ((252, 6.0), (253, 3.0), (254, 1.5)):
+        codes = rng.integers(0, 16, size=(N, K))
+        codes[N // 2:] = rng.choice([c for c in range(16) if [0, .5, 1, 1.5, 2, 3, 4, 6][c & 7] <= largest], size=(N - N // 2, K))
+        scales = np.full((N, K // 32), X, dtype=np.uint8)
+        w, ws = dev(pack(codes)), dev(scales)
+        w64 = decode_mxfp4(pack(codes), scales)
+        y = torch.empty((M, N), dtype=F32, device="cuda")
+        xc = rng.integers(0, 256, size=(M, K // 2)).astype(np.uint8)
+        xs = np.full((M, K // 32), 60, dtype=np.uint8)
+        x64 = decode_mxfp4(xc, xs)
+        mc.mxfp4_matmul(dev(xc), w, ws, y, x_scale=dev(xs))
+        assert (np.abs(y.double().cpu().numpy() - x64 @ w64.T)
+                <= product_bound(x64, w64) + 2.0 ** -24 * np.abs(x64 @ w64.T)).all(), X
+        x = torch.from_numpy(rng.choice([1.0, -1.5, 1.25], size=(M, K)) * 2.0 ** -70).to(BF)
+        x64 = x.double().numpy()
+        mc.mxfp4_matmul(x.cuda(), w, ws, y)
+        got = y.double().cpu().numpy()
+        over = (np.abs(w64) >= 2.0 ** 128).any(axis=1)
+        assert not np.isfinite(got[:, over]).any(), X
+        fits = ~over
+        assert (np.abs(got[:, fits] - x64 @ w64[fits].T)
+                <= product_bound(x64, w64[fits]) + 2.0 ** -24 * np.abs(x64 @ w64[fits].T)).all(), X
+        # read back: what is beyond the type is an infinity
+        for t in (BF, F32):
+            d = torch.empty((N, K), dtype=t, device="cuda")
+            mc.mxfp4_dequantize(w, ws, d)
+            want = np.where(np.abs(w64) >= 2.0 ** 128, np.copysign(np.inf, w64), w64)
+            assert np.array_equal(d.double().cpu().numpy(), want), (X, t)
 
 
 @pytest.mark.parametrize("where", ["cpu", "cuda"])
