@@ -116,6 +116,7 @@ _SIGS = {
     "mc_mxfp4_dequantize": (C.c_int, [_P, _P, _I64, _I64, _P, _I32, _I64, _P]),
     "mc_mxfp4_matmul": (C.c_int, [_P, _P, _I32, _I64, _P, _P, _I32, _I32, _I32, _P, _I32, _I64, _P]),
     "mc_grouped_matmul": (C.c_int, [C.POINTER(Grouped), _P]),
+    "mc_grouped_tile": (C.c_int, [C.POINTER(Grouped), C.POINTER(_I32)]),
     "moe_experts_prefill_act_ws_bytes": (C.c_size_t, [_I32, _I32, _I32, _I32, _I32, _I32]),
     "moe_experts_prefill_act": (C.c_int, [_P, _P, _P, _I32, _I32, _P, _I32, C.POINTER(Banks), _I32, _P,
                                           C.c_size_t, _P, _P, C.POINTER(Prefetch)]),

@@ -1,6 +1,6 @@
 // mc_mxfp4_matmul and mc_grouped_matmul: argument checks and the choice of the operands' formats.
 // The kernels are in product_dev.h, compiled for each pair of formats in a file of its own.
-#include "product.h"
+#include "product_dev.h"
 
 namespace mc {
 
@@ -80,9 +80,7 @@ extern "C" int mc_mxfp4_matmul(const void* x, const void* x_scale, int32_t x_fmt
   return launch_product(a, s);
 }
 
-extern "C" int mc_grouped_matmul(const mc_grouped* g, hipStream_t s) {
-  clear_error();
-  MC_REQUIRE(g != nullptr, "mc_grouped_matmul: descriptor is NULL");
+static ProductArgs grouped_args(const mc_grouped* g) {
   ProductArgs a{};
   a.x = static_cast<const uint8_t*>(g->x);
   a.xs = static_cast<const uint8_t*>(g->x_scale);
@@ -111,6 +109,13 @@ extern "C" int mc_grouped_matmul(const mc_grouped* g, hipStream_t s) {
   a.x_perm = g->x_perm;
   a.y_rows = g->y_rows;
   a.y_perm = g->y_perm;
+  return a;
+}
+
+extern "C" int mc_grouped_matmul(const mc_grouped* g, hipStream_t s) {
+  clear_error();
+  MC_REQUIRE(g != nullptr, "mc_grouped_matmul: descriptor is NULL");
+  const ProductArgs a = grouped_args(g);
   int rc;
   if ((rc = check_product("mc_grouped_matmul", a)) != MC_OK) return rc;
   MC_REQUIRE(a.offsets || a.M == 0, "mc_grouped_matmul: offsets is NULL");
@@ -119,4 +124,18 @@ extern "C" int mc_grouped_matmul(const mc_grouped* g, hipStream_t s) {
   MC_REQUIRE((((int64_t)a.M + 15) / 16) * a.E <= 0x7FFFFFFF, "mc_grouped_matmul: M=%d rows of E=%d groups are too many", a.M,
              a.E);
   return launch_product(a, s);
+}
+
+extern "C" int mc_grouped_tile(const mc_grouped* g, int32_t* tile) {
+  clear_error();
+  MC_REQUIRE(g && tile, "mc_grouped_tile: NULL pointer");
+  const ProductArgs a = grouped_args(g);
+  int rc;
+  if ((rc = check_product("mc_grouped_tile", a)) != MC_OK) return rc;
+  return with_shape(a, [&](auto shape) {
+    typedef decltype(shape) S;
+    if constexpr (std::is_null_pointer_v<S>) tile[0] = 16, tile[1] = 0, tile[2] = 1;
+    else tile[0] = S::BM, tile[1] = S::BN, tile[2] = S::KG;
+    return MC_OK;
+  });
 }

@@ -8,6 +8,8 @@
 // scale byte, so both formats read 16 bytes per lane and 64 per row.
 #pragma once
 
+#include <type_traits>
+
 #include "mxfp4_dev.h"
 #include "product.h"
 
@@ -1025,15 +1027,15 @@ int64_t most_tiles(const ProductArgs& a) {
   return most_row_tiles(a, S::BM) * ((n_out + cols - 1) / cols);
 }
 
-// The kernel for a product's sizes.
-template <int XF, int WF>
-int launch_by_size(const ProductArgs& a, hipStream_t s) {
-  constexpr int MODE = WF == MC_BF16 ? kBf16 : XF == MC_BF16 ? kA16W4 : kFp4;
-  typedef WideShape<2, 4, 4, 8, 1, 1> Big;        // 256 x 256, one workgroup per CU
-  typedef WideShape<2, 2, 4, 4, 1, 2> Medium;     // 128 x 128, two per CU
-  typedef WideShape<2, 2, 4, 4, 2, 1> Medium2;    // 128 x 128, K in two parts
-  typedef WideShape<2, 1, 4, 2, 2, 2> Small2;     // 64 x 64, K in two parts, two per CU
-  typedef WideShape<2, 1, 4, 2, 4, 1> Small4;     // 64 x 64, K in four parts
+typedef WideShape<2, 4, 4, 8, 1, 1> Big;          // 256 x 256, one workgroup per CU
+typedef WideShape<2, 2, 4, 4, 1, 2> Medium;       // 128 x 128, two per CU
+typedef WideShape<2, 2, 4, 4, 2, 1> Medium2;      // 128 x 128, K in two parts
+typedef WideShape<2, 1, 4, 2, 2, 2> Small2;       // 64 x 64, K in two parts, two per CU
+typedef WideShape<2, 1, 4, 2, 4, 1> Small4;       // 64 x 64, K in four parts
+
+// f(a value of the shape's type) for a product's sizes; f(nullptr): tiles of 16 rows (launch_few).
+template <class F>
+int with_shape(const ProductArgs& a, F f) {
   // bytes of a matrix and of x (of a tile's rows of it, if they lie one behind the other), which the
   // wide kernels reach with 32-bit offsets (beyond, the tiles of 16 rows read with 64-bit ones)
   const int64_t w_bytes = (int64_t)a.N * (a.w_fmt == MC_BF16 ? 2 * (int64_t)a.K : a.K / 2);
@@ -1049,17 +1051,28 @@ int launch_by_size(const ProductArgs& a, hipStream_t s) {
     const int64_t groups = a.offsets ? (a.E < a.M ? a.E : a.M) : 1;
     const int64_t n_nb = most_tiles<Big>(a) / most_row_tiles(a, Big::BM);
     const int64_t big = (a.offsets ? a.M / Big::BM + groups / 2 : (a.M + Big::BM - 1) / Big::BM) * n_nb;
-    if (a.M / groups >= 128 && big >= (a.offsets ? 1024 : 192)) return launch_wide<MODE, Big>(a, s);
+    if (a.M / groups >= 128 && big >= (a.offsets ? 1024 : 192)) return f(Big());
     // Too few tiles for the chip: smaller ones, or K shared out among the waves (bf16 rows x MXFP4, us
     // in Small4 / Small2 / Medium: 128 x 4096 x 2048, 128 tiles of 64 x 64, 12 / 16 / 37; 333 x 4100 x
     // 2080, 390 tiles, 34 / 25 / 41; 1000 x 4096 x 2080, 1024 tiles, 61 / 50 / 37 and in Medium2 30).
     const int64_t small = most_tiles<Small4>(a);
-    if (small <= 256) return launch_wide<MODE, Small4>(a, s);
-    if (small <= 768) return launch_wide<MODE, Small2>(a, s);
-    if (most_tiles<Medium2>(a) <= 256) return launch_wide<MODE, Medium2>(a, s);
-    return launch_wide<MODE, Medium>(a, s);
+    if (small <= 256) return f(Small4());
+    if (small <= 768) return f(Small2());
+    if (most_tiles<Medium2>(a) <= 256) return f(Medium2());
+    return f(Medium());
   }
-  return launch_few<XF, WF>(a, s);
+  return f(nullptr);
+}
+
+// The kernel for a product's sizes.
+template <int XF, int WF>
+int launch_by_size(const ProductArgs& a, hipStream_t s) {
+  constexpr int MODE = WF == MC_BF16 ? kBf16 : XF == MC_BF16 ? kA16W4 : kFp4;
+  return with_shape(a, [&](auto shape) {
+    typedef decltype(shape) S;
+    if constexpr (std::is_null_pointer_v<S>) return launch_few<XF, WF>(a, s);
+    else return launch_wide<MODE, S>(a, s);
+  });
 }
 
 }  // namespace mc

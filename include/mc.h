@@ -533,6 +533,13 @@ typedef struct {
 int mc_grouped_matmul(const mc_grouped* g, hipStream_t s);
 
 /*
+ * The tile of such a product (of one of mc_mxfp4_matmul, with offsets NULL), which follows from its sizes
+ * and formats: tile[0] rows of x by tile[1] rows of w, K cut into tile[2] parts of a workgroup;
+ * 16, 0, 1 for the kernel of few rows.  For profiles and tests; enqueues nothing.
+ */
+int mc_grouped_tile(const mc_grouped* g, int32_t* tile);
+
+/*
  * Prefill MoE layer with a choice of activations, for bf16 experts too (moe_experts_prefill
  * is MXFP4 experts on bf16 activations):
  *   y[t] = bf16_rne( sum_j r(w[t][j] * W_down q(silu(W_gate q(x[t])) * (W_up q(x[t])))) )
