@@ -9,7 +9,7 @@
 //
 // The route outputs are fp32, but for act MC_MXFP4, whose caller asked for the shorter buffer: its
 // write and read, 805 MB each way at 8192 tokens x 6 routes x 4096 in fp32, are a quarter of the
-// layer's traffic (layer 1.37 ms with fp32 outputs, 1.27 with bf16).  Each route is then off by up to
+// layer's traffic (layer 1.40 ms with fp32 outputs, 1.24 with bf16).  Each route is then off by up to
 // 2^-8 of itself, which makes the rounding error of y about 1.4 times as large (rms, six routes).
 #include "prefill.h"
 #include "product.h"

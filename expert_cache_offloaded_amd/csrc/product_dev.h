@@ -314,7 +314,8 @@ __device__ __forceinline__ void with_format(const ProductArgs& a, F f) {
 
 __device__ __forceinline__ f32x4_t swiglu4(const f32x4_t& g, const f32x4_t& u) {
   // The division is exact: the reciprocal instruction flushes results below 2^-126 to zero, and with
-  // them silu(g) of g under -87.3, about -1e-36 and a normal number.
+  // them silu(g) of g under -87.3, about -1e-36 and a normal number (layer of 8192 tokens 1.39 ms with
+  // the reciprocal, 1.41 so).
   f32x4_t h;
 #pragma unroll
   for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i];
@@ -475,7 +476,13 @@ product_few_kernel(ProductArgs a, int n_nb, uint32_t tiles) {
 // without its loads and 1.3 without its products, which are 0.9 us of MFMA time at 2.2 GHz: the LDS
 // serves 192 KiB of operands, 24 of scales and 72 of arriving data in it.  A wave tile of 128 x 128
 // (one wave per SIMD) reads a third less and took 2.3 us a stage; 64-byte stages four deep 1.7
-// times as many L2 requests and 106 against 92 us a product.
+// times as many L2 requests and 106 against 92 us a product.  That is one dense product, all of whose
+// tiles run the same code.  Every form of results is compiled into every number of row fragments:
+// the 256 x 256 kernels have 470-485 KB of code, those of 128 x 128 130-148 and those of 64 x 64 44-48,
+// the first two of more than the instruction cache holds, so groups of uneven sizes, whose
+// tiles differ in fragments, fetch each epilogue anew; what that costs has not been measured.  The
+// 256 x 256 kernels with MXFP4 weights fill all 256 VGPRs and spill up to 6 of them, and they and
+// the 128 x 128 ones without K groups keep 83-113 SGPRs in lanes of VGPRs.
 
 enum { kBf16 = 0, kA16W4 = 1, kFp4 = 2 };
 
@@ -559,7 +566,9 @@ struct WideLds {
 };
 
 // The stages of a row that a K group takes: from `from` on, `n` of them (`most` in the first group,
-// which has the most).
+// which has the most).  Shares are multiples of what the weights or the scales come in for, so they are
+// uneven, and groups of a short row get nothing: bf16 x MXFP4 takes K = 2080 in 20 and 13 stages,
+// or in 12, 12, 9 and none, and K = 512 whole.
 template <int MODE, class S, bool SDMA>
 struct WideShare {
   int from, n, most;
@@ -945,6 +954,8 @@ product_wide_kernel(ProductArgs a, int n_nb) {
     auto run = [&](auto mf) {
       wide_tile<MODE, S, SDMA, decltype(mf)::value>(a, n_nb, lds, t, src, turn, sc, more, b, total, next, wdst, xdst, sdst);
     };
+    // without direct scales two forms only, which keep the 256 x 256 kernel at 161 instead of 485 KB
+    // of code: a tile of 150 rows then computes 256
     if constexpr (!SDMA || S::MFX == 2) {
       if (2 * steps <= S::MFX) run(Const<S::MFX / 2>());
       else run(Const<S::MFX>());
@@ -1042,7 +1053,9 @@ int with_shape(const ProductArgs& a, F f) {
   const int64_t x_bytes = (a.x_perm ? a.x_rows : Big::BM) * (a.x_fmt == MC_BF16 ? 2 * a.ldx : a.K / 2);
   // Up to 16 rows: one token's experts 8 us (12 in Small4), 8 x 4096 x 4096 7 us (16); from 17 rows on
   // Small4 is level or ahead (17 x 4096 x 2048 bf16: 8 against 12 us, 64 x 4096 x 4096: 19 against
-  // 35 us).
+  // 35 us; products of one group.  Of grouped ones both sides have not been compared: with eight
+  // routes a token, bf16 x MXFP4 1024 x 2048, 2 tokens take 11 us in tiles of 16 rows, 3 take 18, 4 18
+  // and 8 32 in the others).
   if (a.M > 16 && w_bytes <= UINT32_MAX && x_bytes <= UINT32_MAX) {
     // The large tiles read each operand half as often, and win where they fill the chip with full
     // tiles: 8192 x 4096 x 4096 in fp4 86 against 101 us, 256 experts of 192 rows 1.40 against
@@ -1054,7 +1067,9 @@ int with_shape(const ProductArgs& a, F f) {
     if (a.M / groups >= 128 && big >= (a.offsets ? 1024 : 192)) return f(Big());
     // Too few tiles for the chip: smaller ones, or K shared out among the waves (bf16 rows x MXFP4, us
     // in Small4 / Small2 / Medium: 128 x 4096 x 2048, 128 tiles of 64 x 64, 12 / 16 / 37; 333 x 4100 x
-    // 2080, 390 tiles, 34 / 25 / 41; 1000 x 4096 x 2080, 1024 tiles, 61 / 50 / 37 and in Medium2 30).
+    // 2080, 390 tiles, 34 / 25 / 41; 1000 x 4096 x 2080, 1024 tiles, 61 / 50 / 37 and in Medium2 30).  At
+    // K = 2080 one of Small4's four groups is without work, and the halves of the others are 20 and
+    // 13 stages.
     const int64_t small = most_tiles<Small4>(a);
     if (small <= 256) return f(Small4());
     if (small <= 768) return f(Small2());
